@@ -69,7 +69,8 @@ typedef enum {
   THETA_OP_RESIDUAL_SVD = 3,
   THETA_OP_NVFP4_QUANTIZE = 4,
   THETA_OP_LINEAR_FORWARD_NVFP4 = 5,
-  THETA_OP_LINEAR_FORWARD_GROUPED = 6
+  THETA_OP_LINEAR_FORWARD_GROUPED = 6,
+  THETA_OP_LINEAR_FORWARD_FP8 = 7
 } theta_op;
 
 /* How the tensor-core kernels size their grids (see theta_set_policy). */
@@ -375,6 +376,93 @@ int theta_linear_forward_grouped(const theta_forward_problem* problems, const th
 int theta_linear_forward_nvfp4(const void* X, int64_t M, int64_t I, const void* codes, const void* scales,
                                const float* g, int64_t O, const float* s, const void* U, const void* V, int rank,
                                void* Y, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * theta_fp8_quantize -- encodes a shared block W0 in 8 bits for
+ * theta_linear_forward_fp8 (a library format; the pages describe none): E4M3
+ * codes with one power-of-two scale per 128 x 128 block, 1.00006 bytes per
+ * weight. Per block, with a = max |w| over its finite values:
+ *   e = the least integer >= -127 with a <= 448 * 2^e (0 if a == 0);
+ *   scale byte = e + 127 (E8M0);
+ *   code = E4M3(w * 2^-e), round-to-nearest-even; the weight it stands for is
+ *   E4M3value(code) * 2^e.
+ * A value that is not finite gets the NaN code 0x7f and does not count for a.
+ * Blocks at the right and bottom edge cover what is left of the matrix.
+ *
+ *   W0 [O, I] of dt; codes uint8 [O, I], written; scales uint8
+ *   [ceil(O/128), ceil(I/128)], written. I a multiple of 16, W0 and codes
+ *   16-byte aligned (else THETA_ERR_ALIGNMENT). W0 and codes must not overlap.
+ */
+int theta_fp8_quantize(const void* W0, int64_t O, int64_t I, theta_dtype dt, void* codes, void* scales,
+                       void* stream);
+
+/*
+ * theta_fp8_quantize_rows -- the same encoding of activations X [M, I], one
+ * scale per token and block of 128 columns, for theta_linear_forward_fp8.
+ * Projections that share an input (q, k and v; gate and up) share its codes.
+ *
+ *   X [M, I] of dt; codes uint8 [M, I], written; scales uint8
+ *   [ceil(I/128), M], written: one row per block of columns, so that the
+ *   scales of neighbouring tokens are neighbours. Rules as theta_fp8_quantize.
+ */
+int theta_fp8_quantize_rows(const void* X, int64_t M, int64_t I, theta_dtype dt, void* codes, void* scales,
+                            void* stream);
+
+/*
+ * theta_linear_forward_fp8 -- theta_linear_forward with the shared block and
+ * the activations in 8 bits (from theta_fp8_quantize and
+ * theta_fp8_quantize_rows), for any number of tokens:
+ *   Y = s (.) (Xq . W0q^T) + (X . V) . U^T
+ * with Xq and W0q the values that the codes stand for. The rank-r correction
+ * is formed from the bf16 X, so it keeps its precision.
+ *
+ *   X [M, I] bf16 (read for the rank-r term only; may be NULL when rank == 0);
+ *   X_codes, X_scales, codes, scales as the two encoders write them; s fp32
+ *   [O]; U [O, rank], V [I, rank] bf16; Y [M, O] bf16, written.
+ *   M, I, O >= 1; 0 <= rank <= 256; I a multiple of 16, O and rank multiples
+ *   of 8, every pointer but the scales 16-byte aligned (else
+ *   THETA_ERR_ALIGNMENT). M, O, I < 2^30, M and O at most 4,194,240 (else
+ *   THETA_ERR_UNSUPPORTED).
+ *   workspace: theta_workspace_size(THETA_OP_LINEAR_FORWARD_FP8, M, O, I,
+ *   rank, THETA_BF16) bytes (holds T = X . V; 0 at rank 0).
+ */
+int theta_linear_forward_fp8(const void* X, const void* X_codes, const void* X_scales, int64_t M, int64_t I,
+                             const void* codes, const void* scales, int64_t O, const float* s, const void* U,
+                             const void* V, int rank, void* Y, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * theta_qk_norm_rope -- what the Gemma decoders do to the outputs of the q
+ * and k projections before attention: an RMS norm of every head and the
+ * position rotation, in one pass. (No counterpart on the pages; the
+ * attention family's counterpart of the activation in
+ * theta_linear_gate_up_forward.) For each token m and head of D = head_dim
+ * values x:
+ *   h = x / sqrt(mean(x^2) + eps) * (weight + weight_offset)
+ *   pairs (a, b) of the first rotary_dim values, t = positions[m] * inv_freq[i]:
+ *   y_a = h_a cos t - h_b sin t,  y_b = h_b cos t + h_a sin t
+ * with (a, b) = (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved,
+ * i < rotary_dim / 2; the other values are y = h. fp32 arithmetic, one
+ * rounding to dt; angles in fp64 (at |position| < 2^31 an error below 2^-19
+ * radian, falling with the position).
+ *
+ *   Q  rows of q_heads * D values, ldq elements apart (a projection's Y: ldq =
+ *      q_heads * D; a slice of a fused q/k/v output: that output's width).
+ *   K  likewise with k_heads; k_heads == 0 skips it (K, K_out may be NULL).
+ *   q_weight, k_weight  [D] of dt, or NULL for a norm without weight (the
+ *      factor is then 1 and weight_offset is not used). weight_offset is 1
+ *      for checkpoints that store w - 1.
+ *   positions int64 [M], inv_freq fp32 [rotary_dim / 2]: device; may be NULL
+ *      when rotary_dim == 0 (norm only).
+ *   Q_out, K_out  written; ldq_out, ldk_out elements apart. Each may be its
+ *      own input (same pointer, same pitch); any other overlap is not allowed.
+ *   1 <= M <= 2^30; D a multiple of 8, at most 1024; rotary_dim even, 0 ..
+ *   D; q_heads, k_heads <= 65535; pitches at least the row (M > 1) and
+ *   multiples of 8; base pointers 16-byte aligned; eps >= 0.
+ */
+int theta_qk_norm_rope(const void* Q, int64_t ldq, int q_heads, const void* K, int64_t ldk, int k_heads, int64_t M,
+                       int head_dim, theta_dtype dt, const void* q_weight, const void* k_weight, float weight_offset,
+                       float eps, const int64_t* positions, const float* inv_freq, int rotary_dim, int interleaved,
+                       void* Q_out, int64_t ldq_out, void* K_out, int64_t ldk_out, void* stream);
 
 /*
  * theta_linear_forward_noalloc -- theta_linear_forward for callers that

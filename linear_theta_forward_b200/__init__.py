@@ -19,6 +19,8 @@ __all__ = [
     "THETA_OP_NVFP4_QUANTIZE", "THETA_OP_LINEAR_FORWARD_NVFP4", "theta_nvfp4_quantize", "theta_linear_forward_nvfp4",
     "THETA_MAX_LAYERS", "LIB_PATH", "lib", "THETA_OP_LINEAR_FORWARD_GROUPED", "THETA_MAX_GROUP",
     "theta_forward_problem", "ForwardGroup", "theta_linear_forward_grouped",
+    "THETA_OP_LINEAR_FORWARD_FP8", "theta_fp8_quantize", "theta_fp8_quantize_rows", "theta_linear_forward_fp8",
+    "theta_qk_norm_rope",
     "theta_version", "theta_status_string", "theta_last_error", "theta_band_index",
     "theta_band_mean", "theta_row_scale", "theta_residual", "theta_decompose_prelude",
     "theta_reconstruct", "theta_reconstruct_band", "theta_frob_error", "theta_frob_partials", "theta_linear_forward", "theta_workspace_size",
@@ -30,7 +32,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtheta.so
 
 THETA_F32, THETA_BF16 = 0, 1
 (THETA_OP_FROB_ERROR, THETA_OP_LINEAR_FORWARD, THETA_OP_GATE_UP_FORWARD, THETA_OP_RESIDUAL_SVD, THETA_OP_NVFP4_QUANTIZE,
- THETA_OP_LINEAR_FORWARD_NVFP4, THETA_OP_LINEAR_FORWARD_GROUPED) = 0, 1, 2, 3, 4, 5, 6
+ THETA_OP_LINEAR_FORWARD_NVFP4, THETA_OP_LINEAR_FORWARD_GROUPED, THETA_OP_LINEAR_FORWARD_FP8) = range(8)
 THETA_POLICY_LATENCY, THETA_POLICY_THROUGHPUT = 0, 1
 THETA_MAX_LAYERS = 256
 THETA_MAX_GROUP = 256
@@ -62,6 +64,12 @@ _SIGNATURES = {
     "theta_nvfp4_quantize": (_int, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp),
     "theta_linear_forward_nvfp4": (_int, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _int, _vp, _vp, _sz,
                                    _vp),
+    "theta_fp8_quantize": (_int, _vp, _i64, _i64, _int, _vp, _vp, _vp),
+    "theta_fp8_quantize_rows": (_int, _vp, _i64, _i64, _int, _vp, _vp, _vp),
+    "theta_linear_forward_fp8": (_int, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _int, _vp, _vp, _sz,
+                                 _vp),
+    "theta_qk_norm_rope": (_int, _vp, _i64, _int, _vp, _i64, _int, _i64, _int, _int, _vp, _vp, ctypes.c_float,
+                           ctypes.c_float, _vp, _vp, _int, _int, _vp, _i64, _vp, _i64, _vp),
     "theta_residual_svd": (_int, _vp, _i64, _i64, _int, _int, _int, _int, _vp, _vp, _vp, _vp, _sz, _vp),
     "theta_linear_gate_up_forward": (_int, _vp, _i64, _i64, _i64, _int, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                      _vp, _vp, _sz, _vp),
@@ -360,6 +368,109 @@ def theta_linear_forward_nvfp4(X, codes, scales, g, s, U, V, Y, workspace=None, 
                                               _ptr(V, "V", optional=True), rank, _ptr(Y, "Y"), ws_ptr, ws_bytes,
                                               _stream(stream)),
            "theta_linear_forward_nvfp4")
+
+
+def _typed(t, name, dtype, shape, device=None):
+    """A CUDA tensor's pointer, after its dtype, shape, layout and device (an
+    ordinal; None: the current one) have been checked."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    p = _ptr(t, name)
+    _on_device(t, name, device)
+    return p
+
+
+def _on_device(t, name, device=None):
+    """The calls work on the current device: a pointer of another one would fault there."""
+    now = _torch().cuda.current_device() if device is None else device
+    if t.get_device() != now:
+        raise ValueError(f"{name} is on device {t.get_device()}, the current device is {now}")
+
+
+def theta_fp8_quantize(W0, codes, scales, stream=None) -> None:
+    """Encode W0 [O, I] (bf16 or fp32) in E4M3: codes uint8 [O, I], scales
+    uint8 [ceil(O/128), ceil(I/128)], one power of two per 128 x 128 block."""
+    torch = _torch()
+    O, I = W0.shape
+    _check(_load().theta_fp8_quantize(_typed(W0, "W0", W0.dtype, (O, I)), O, I, _dtype_code(W0),
+                                      _typed(codes, "codes", torch.uint8, (O, I)),
+                                      _typed(scales, "scales", torch.uint8, (-(-O // 128), -(-I // 128))),
+                                      _stream(stream)), "theta_fp8_quantize")
+
+
+def theta_fp8_quantize_rows(X, codes, scales, stream=None) -> None:
+    """Encode activations X [M, I] (bf16 or fp32) in E4M3: codes uint8 [M, I],
+    scales uint8 [ceil(I/128), M], one power of two per token and 128 columns."""
+    torch = _torch()
+    M, I = X.shape
+    _check(_load().theta_fp8_quantize_rows(_typed(X, "X", X.dtype, (M, I)), M, I, _dtype_code(X),
+                                           _typed(codes, "codes", torch.uint8, (M, I)),
+                                           _typed(scales, "scales", torch.uint8, (-(-I // 128), M)),
+                                           _stream(stream)), "theta_fp8_quantize_rows")
+
+
+def theta_linear_forward_fp8(X, X_codes, X_scales, codes, scales, s, U, V, Y, workspace=None, stream=None) -> None:
+    """Y [M, O] = s * (Xq W0q^T) + (X V) U^T, Xq and W0q what theta_fp8_quantize_rows
+    and theta_fp8_quantize wrote. X (bf16) may be None when U and V are.
+    workspace: CUDA tensor of at least theta_workspace_size(
+    THETA_OP_LINEAR_FORWARD_FP8, ...) bytes (None if 0)."""
+    torch = _torch()
+    u8, bf = torch.uint8, torch.bfloat16
+    M, I = X_codes.shape
+    O = codes.shape[0]
+    nb = -(-I // 128)
+    rank = 0 if U is None else U.shape[1]
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        ws_ptr, ws_bytes = _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
+        _on_device(workspace, "workspace")
+    if (U is None) != (V is None):
+        raise ValueError("U and V must be given together")
+    _check(_load().theta_linear_forward_fp8(
+        None if X is None else _typed(X, "X", bf, (M, I)), _typed(X_codes, "X_codes", u8, (M, I)),
+        _typed(X_scales, "X_scales", u8, (nb, M)), M, I, _typed(codes, "codes", u8, (O, I)),
+        _typed(scales, "scales", u8, (-(-O // 128), nb)), O, _typed(s, "s", torch.float32, (O,)),
+        None if U is None else _typed(U, "U", bf, (O, rank)), None if V is None else _typed(V, "V", bf, (I, rank)),
+        rank, _typed(Y, "Y", bf, (M, O)), ws_ptr, ws_bytes, _stream(stream)), "theta_linear_forward_fp8")
+
+
+def _rows(t, name, M, head_dim, dtype):
+    """(pointer, row pitch, heads) of a [M, heads * head_dim] tensor whose rows are dense (the pitch may be larger)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != M or t.shape[1] % head_dim or t.stride(1) != 1:
+        raise ValueError(f"{name} must be {dtype} [{M}, heads * {head_dim}] with dense rows, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+    _on_device(t, name)
+    return t.data_ptr(), t.stride(0) if M > 1 else t.shape[1], t.shape[1] // head_dim
+
+
+def theta_qk_norm_rope(Q, K, q_weight, k_weight, positions, inv_freq, Q_out, K_out, head_dim, eps=1e-6,
+                       weight_offset=0.0, interleaved=False, stream=None) -> None:
+    """RMS norm of every head of Q [M, q_heads * head_dim] and K [M, k_heads *
+    head_dim] times (weight + weight_offset), then the rotation of each head's
+    first 2 * len(inv_freq) values by positions (int64 [M]) * inv_freq (fp32).
+    K and K_out, each weight, and positions with inv_freq may be None. Rows
+    may be slices of a wider tensor; Q_out and K_out may be Q and K."""
+    torch = _torch()
+    head_dim = int(head_dim)
+    if head_dim < 1:
+        raise ValueError("head_dim must be positive")
+    M, dtype = Q.shape[0], Q.dtype
+    q, ldq, nq = _rows(Q, "Q", M, head_dim, dtype)
+    qo, ldqo, nqo = _rows(Q_out, "Q_out", M, head_dim, dtype)
+    k, ldk, nk = (None, 0, 0) if K is None else _rows(K, "K", M, head_dim, dtype)
+    ko, ldko, nko = (None, 0, 0) if K_out is None else _rows(K_out, "K_out", M, head_dim, dtype)
+    if nqo != nq or nko != nk:
+        raise ValueError("Q_out and K_out must have as many heads as Q and K")
+    half = 0 if inv_freq is None else inv_freq.numel()
+    _check(_load().theta_qk_norm_rope(
+        q, ldq, nq, k, ldk, nk, M, head_dim, _dtype_code(Q),
+        None if q_weight is None else _typed(q_weight, "q_weight", dtype, (head_dim,)),
+        None if k_weight is None else _typed(k_weight, "k_weight", dtype, (head_dim,)), weight_offset, eps,
+        None if positions is None else _typed(positions, "positions", torch.int64, (M,)),
+        None if inv_freq is None else _typed(inv_freq, "inv_freq", torch.float32, (half,)), 2 * half,
+        int(interleaved), qo, ldqo, ko, ldko, _stream(stream)), "theta_qk_norm_rope")
 
 
 def theta_residual_svd(R, rank, omega, U, V, workspace, power_iters=2, stream=None) -> None:

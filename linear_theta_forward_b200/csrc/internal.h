@@ -88,6 +88,34 @@ bool launch_forward_nvfp4(const LaunchCtx& c, const void* X, const void* codes, 
                           const float* s, const void* U, const void* V, int64_t M, int64_t O, int64_t I, int r,
                           void* Y, void* ws, cudaError_t* e);
 
+// ---- block-scaled FP8 (fp8_kernels.cu): E4M3 codes and E8M0 scales of W0
+// (one per 128 x 128 block, [ceil(O/128), ceil(I/128)]) and of activation rows
+// (one per token and 128 columns, [ceil(I/128), M]); the forward over both.
+constexpr int kFp8Block = 128;
+constexpr int64_t kFp8MaxSize = ((int64_t)1 << 30) - 1;  // of I, and of the encoders' rows
+cudaError_t launch_fp8_quantize(const LaunchCtx& c, theta_dtype dt, const void* W, int64_t O, int64_t I, void* codes,
+                                void* scales);
+cudaError_t launch_fp8_quantize_rows(const LaunchCtx& c, theta_dtype dt, const void* X, int64_t M, int64_t I,
+                                     void* codes, void* scales);
+size_t forward_fp8_workspace_bytes(int64_t M, int r);
+int launch_forward_fp8(const LaunchCtx& c, const void* X, const void* xq, const void* xs, const void* wq,
+                       const void* ws, const float* s, const void* U, const void* V, int64_t M, int64_t O, int64_t I,
+                       int r, void* Y, void* work, cudaError_t* ce);
+
+// ---- per-head norm and rotation (heads_kernels.cu): one side's heads, rows
+// of `ld` elements in and `ld_out` out, an optional weight of head_dim values.
+struct HeadSide {
+  const void* x;
+  void* y;
+  const void* weight;
+  int64_t ld, ld_out;
+  int heads;
+};
+int heads_max_dim();
+cudaError_t launch_qk_norm_rope(const LaunchCtx& c, theta_dtype dt, const HeadSide& q, const HeadSide& k, int64_t M,
+                                int head_dim, float offset, float eps, const int64_t* positions,
+                                const float* inv_freq, int rotary, bool interleaved);
+
 // ---- randomized SVD of a residual (svd_kernels.cu): R [O, I] in dt, omega
 // fp32 [samples, I]; U [O, rank], V [I, rank] in dt; ws of svd_workspace_bytes.
 int svd_max_samples();

@@ -537,6 +537,107 @@ THETA_API int theta_linear_forward_nvfp4(const void* X, int64_t M, int64_t I, co
   return THETA_OK;
 }
 
+THETA_API int theta_fp8_quantize(const void* W0, int64_t O, int64_t I, theta_dtype dt, void* codes, void* scales,
+                                 void* stream) {
+  if (!valid_dt(dt)) return fail(THETA_ERR_INVALID_ARG, "theta_fp8_quantize: bad dtype %d", (int)dt);
+  if (O < 1 || I < 1) return fail(THETA_ERR_INVALID_ARG, "theta_fp8_quantize: O, I must be >= 1");
+  if (!W0 || !codes || !scales) return fail(THETA_ERR_INVALID_ARG, "theta_fp8_quantize: NULL pointer");
+  if (!aligned16(W0) || !aligned16(codes) || I % 16)
+    return fail(THETA_ERR_ALIGNMENT, "theta_fp8_quantize: W0 and codes 16-byte aligned, I a multiple of 16");
+  if (O > kFp8MaxSize || I > kFp8MaxSize || ceil_div(O, kFp8Block) * ceil_div(I, kFp8Block) > INT32_MAX)
+    return fail(THETA_ERR_UNSUPPORTED, "theta_fp8_quantize: too many blocks of 128 x 128");
+  LaunchCtx c;
+  int st = make_ctx(stream, &c);
+  if (st) return st;
+  CHECK_LAUNCH(launch_fp8_quantize(c, dt, W0, O, I, codes, scales), "theta_fp8_quantize launch");
+  return THETA_OK;
+}
+
+THETA_API int theta_fp8_quantize_rows(const void* X, int64_t M, int64_t I, theta_dtype dt, void* codes, void* scales,
+                                      void* stream) {
+  if (!valid_dt(dt)) return fail(THETA_ERR_INVALID_ARG, "theta_fp8_quantize_rows: bad dtype %d", (int)dt);
+  if (M < 1 || I < 1) return fail(THETA_ERR_INVALID_ARG, "theta_fp8_quantize_rows: M, I must be >= 1");
+  if (!X || !codes || !scales) return fail(THETA_ERR_INVALID_ARG, "theta_fp8_quantize_rows: NULL pointer");
+  if (!aligned16(X) || !aligned16(codes) || I % 16)
+    return fail(THETA_ERR_ALIGNMENT, "theta_fp8_quantize_rows: X and codes 16-byte aligned, I a multiple of 16");
+  if (M > kFp8MaxSize || I > kFp8MaxSize || M * ceil_div(I, kFp8Block) > INT32_MAX)
+    return fail(THETA_ERR_UNSUPPORTED, "theta_fp8_quantize_rows: too many blocks of 128 columns");
+  LaunchCtx c;
+  int st = make_ctx(stream, &c);
+  if (st) return st;
+  CHECK_LAUNCH(launch_fp8_quantize_rows(c, dt, X, M, I, codes, scales), "theta_fp8_quantize_rows launch");
+  return THETA_OK;
+}
+
+THETA_API int theta_linear_forward_fp8(const void* X, const void* X_codes, const void* X_scales, int64_t M, int64_t I,
+                                       const void* codes, const void* scales, int64_t O, const float* s,
+                                       const void* U, const void* V, int rank, void* Y, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  if (M < 1 || I < 1 || O < 1 || rank < 0 || rank > 256)
+    return fail(THETA_ERR_INVALID_ARG, "theta_linear_forward_fp8: need M, I, O >= 1 and 0 <= rank <= 256");
+  if (!X_codes || !X_scales || !codes || !scales || !s || !Y || (rank > 0 && (!X || !U || !V)))
+    return fail(THETA_ERR_INVALID_ARG, "theta_linear_forward_fp8: NULL pointer");
+  for (const void* p : {X_codes, codes, static_cast<const void*>(s), static_cast<const void*>(Y)})
+    if (!aligned16(p)) return fail(THETA_ERR_ALIGNMENT, "theta_linear_forward_fp8: needs 16-byte aligned pointers");
+  if ((rank > 0 && (!aligned16(X) || !aligned16(U) || !aligned16(V))) || I % 16 || O % 8 || rank % 8)
+    return fail(THETA_ERR_ALIGNMENT,
+                "theta_linear_forward_fp8: 16-byte aligned pointers, I a multiple of 16, O and rank of 8");
+  if (M > kSimtMaxRows || O > kSimtMaxRows || I > kFp8MaxSize)
+    return fail(THETA_ERR_UNSUPPORTED, "theta_linear_forward_fp8: M and O must be <= %lld, I <= %lld",
+                (long long)kSimtMaxRows, (long long)kFp8MaxSize);
+  const size_t need = align_up(forward_fp8_workspace_bytes(M, rank), 256);
+  if (need && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+    return fail(THETA_ERR_WORKSPACE, "theta_linear_forward_fp8: need %zu bytes of 16-byte aligned workspace", need);
+  LaunchCtx c;
+  int st = make_ctx(stream, &c);
+  if (st) return st;
+  cudaError_t ce = cudaSuccess;
+  st = launch_forward_fp8(c, X, X_codes, X_scales, codes, scales, s, U, V, M, O, I, rank, Y, workspace, &ce);
+  if (st == THETA_ERR_CUDA) return fail_cuda(ce, "theta_linear_forward_fp8 launch");
+  return st;
+}
+
+THETA_API int theta_qk_norm_rope(const void* Q, int64_t ldq, int q_heads, const void* K, int64_t ldk, int k_heads,
+                                 int64_t M, int head_dim, theta_dtype dt, const void* q_weight, const void* k_weight,
+                                 float weight_offset, float eps, const int64_t* positions, const float* inv_freq,
+                                 int rotary_dim, int interleaved, void* Q_out, int64_t ldq_out, void* K_out,
+                                 int64_t ldk_out, void* stream) {
+  if (!valid_dt(dt)) return fail(THETA_ERR_INVALID_ARG, "theta_qk_norm_rope: bad dtype %d", (int)dt);
+  if (M < 1 || M > (int64_t)1 << 30 || q_heads < 1 || q_heads > 65535 || k_heads < 0 || k_heads > 65535)
+    return fail(THETA_ERR_INVALID_ARG,
+                "theta_qk_norm_rope: need 1 <= M <= 2^30, 1 <= q_heads <= 65535, 0 <= k_heads <= 65535");
+  if (head_dim < 8 || head_dim % 8 || rotary_dim < 0 || rotary_dim > head_dim || rotary_dim % 2 || !(eps >= 0.f))
+    return fail(THETA_ERR_INVALID_ARG,
+                "theta_qk_norm_rope: need head_dim a multiple of 8, rotary_dim even and in [0, head_dim], eps >= 0");
+  if (head_dim > heads_max_dim())
+    return fail(THETA_ERR_UNSUPPORTED, "theta_qk_norm_rope: head_dim must be <= %d", heads_max_dim());
+  if (!Q || !Q_out || (k_heads > 0 && (!K || !K_out)) || (rotary_dim > 0 && (!positions || !inv_freq)))
+    return fail(THETA_ERR_INVALID_ARG, "theta_qk_norm_rope: NULL pointer");
+  const HeadSide side[2] = {{Q, Q_out, q_weight, ldq, ldq_out, q_heads}, {K, K_out, k_weight, ldk, ldk_out, k_heads}};
+  for (const HeadSide& h : side) {
+    if (h.heads == 0) continue;
+    const int64_t row = (int64_t)h.heads * head_dim;
+    if (M > 1 && (h.ld < row || h.ld_out < row))
+      return fail(THETA_ERR_INVALID_ARG, "theta_qk_norm_rope: a row pitch is below heads * head_dim = %lld",
+                  (long long)row);
+    if (h.x == h.y && M > 1 && h.ld != h.ld_out)
+      return fail(THETA_ERR_INVALID_ARG, "theta_qk_norm_rope: in place needs equal pitches");
+    if (!aligned16(h.x) || !aligned16(h.y) || h.ld % 8 || h.ld_out % 8)
+      return fail(THETA_ERR_ALIGNMENT,
+                  "theta_qk_norm_rope: Q, K, Q_out, K_out 16-byte aligned, pitches multiples of 8");
+  }
+  if (rotary_dim > 0 &&
+      ((reinterpret_cast<uintptr_t>(positions) & 7u) != 0 || (reinterpret_cast<uintptr_t>(inv_freq) & 3u) != 0))
+    return fail(THETA_ERR_ALIGNMENT, "theta_qk_norm_rope: positions 8-byte, inv_freq 4-byte aligned");
+  LaunchCtx c;
+  int st = make_ctx(stream, &c);
+  if (st) return st;
+  CHECK_LAUNCH(launch_qk_norm_rope(c, dt, side[0], side[1], M, head_dim, weight_offset, eps, positions, inv_freq,
+                                   rotary_dim, interleaved != 0),
+               "theta_qk_norm_rope launch");
+  return THETA_OK;
+}
+
 THETA_API int theta_workspace_size(int op, int64_t M, int64_t O, int64_t I, int rank, theta_dtype dt,
                                    size_t* bytes) {
   if (!bytes) return fail(THETA_ERR_INVALID_ARG, "theta_workspace_size: bytes is NULL");
@@ -557,6 +658,10 @@ THETA_API int theta_workspace_size(int op, int64_t M, int64_t O, int64_t I, int 
     case THETA_OP_LINEAR_FORWARD_NVFP4:
       if (M < 1 || rank < 0 || I < 1) return fail(THETA_ERR_INVALID_ARG, "theta_workspace_size: bad M, I or rank");
       *bytes = forward_nvfp4_workspace_bytes(M, I, rank);
+      return THETA_OK;
+    case THETA_OP_LINEAR_FORWARD_FP8:
+      if (M < 1 || rank < 0 || rank > 256) return fail(THETA_ERR_INVALID_ARG, "theta_workspace_size: bad M or rank");
+      *bytes = align_up(forward_fp8_workspace_bytes(M, rank), 256);
       return THETA_OK;
     case THETA_OP_LINEAR_FORWARD_GROUPED:  // O carries the problem count, rank the largest rank
       if (M < 1 || M > 2 || O < 1 || O > THETA_MAX_GROUP || rank < 0 || rank > 256)

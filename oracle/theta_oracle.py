@@ -247,6 +247,101 @@ def linear_forward_nvfp4(X, codes, scales, g, s, U, V, out_dtype: str = "f64") -
     return linear_forward(X, nvfp4_dequantize(codes, scales, g), s, U, V, out_dtype)
 
 
+# ------------------------------------------------------- block-scaled FP8
+# E4M3 codes with one power of two (E8M0: exponent + 127) per block of 128:
+# 128 x 128 of a shared block, one token x 128 columns of activations.
+def _fp8_exponent(a):
+    """The least integer e >= -127 with a <= 448 * 2^e; 0 for a == 0."""
+    if a == 0:
+        return 0
+    e = -127
+    while a > 448.0 * 2.0 ** e:
+        e += 1
+    return e
+
+
+def _fp8_block(x):
+    """(codes, scale byte) of one block of fp64 values."""
+    fine = np.isfinite(x)
+    e = _fp8_exponent(float(np.max(np.abs(x), where=fine, initial=0.0)))
+    v = np.where(fine, x, 0.0) * 2.0 ** -e
+    code = _grid_round(np.abs(v), e4m3_values()) | np.where(np.signbit(v), 128, 0)
+    return np.where(fine, code, 127).astype(np.uint8), np.uint8(e + 127)
+
+
+def fp8_quantize(W):
+    """W [O, I] -> (codes uint8 [O, I], scales uint8 [ceil(O/128), ceil(I/128)])."""
+    w = np.asarray(W, dtype=F64)
+    O, I = w.shape
+    codes = np.zeros((O, I), np.uint8)
+    scales = np.zeros((-(-O // 128), -(-I // 128)), np.uint8)
+    for a in range(scales.shape[0]):
+        for b in range(scales.shape[1]):
+            at = np.s_[a * 128:(a + 1) * 128, b * 128:(b + 1) * 128]
+            codes[at], scales[a, b] = _fp8_block(w[at])
+    return codes, scales
+
+
+def fp8_quantize_rows(X):
+    """X [M, I] -> (codes uint8 [M, I], scales uint8 [ceil(I/128), M])."""
+    x = np.asarray(X, dtype=F64)
+    M, I = x.shape
+    codes = np.zeros((M, I), np.uint8)
+    scales = np.zeros((-(-I // 128), M), np.uint8)
+    for m in range(M):
+        for b in range(scales.shape[0]):
+            codes[m, b * 128:(b + 1) * 128], scales[b, m] = _fp8_block(x[m, b * 128:(b + 1) * 128])
+    return codes, scales
+
+
+def fp8_values(codes) -> np.ndarray:
+    """The fp64 values of E4M3 codes (NaN for 0x7f and 0xff)."""
+    c = np.asarray(codes, dtype=np.int64)
+    mag = np.append(e4m3_values(), np.nan)[c & 127]
+    return np.where(c & 128, -mag, mag)
+
+
+def fp8_dequantize(codes, scales) -> np.ndarray:
+    """The fp64 shared block that fp8_quantize's output stands for."""
+    O, I = np.asarray(codes).shape
+    p = np.exp2(np.asarray(scales, dtype=F64) - 127.0)
+    return fp8_values(codes) * np.repeat(np.repeat(p, 128, axis=0)[:O], 128, axis=1)[:, :I]
+
+
+def fp8_dequantize_rows(codes, scales) -> np.ndarray:
+    """The fp64 activations that fp8_quantize_rows's output stands for."""
+    I = np.asarray(codes).shape[1]
+    p = np.exp2(np.asarray(scales, dtype=F64) - 127.0)
+    return fp8_values(codes) * np.repeat(p.T, 128, axis=1)[:, :I]
+
+
+def linear_forward_fp8(X, x_codes, x_scales, codes, scales, s, U, V) -> np.ndarray:
+    """s (.) (Xq . W0q^T) + (X . V) . U^T in fp64, Xq and W0q from their encodings."""
+    xq, wq = fp8_dequantize_rows(x_codes, x_scales), fp8_dequantize(codes, scales)
+    y = (xq @ wq.T) * np.asarray(s, dtype=F64)
+    if U is not None and np.asarray(U).size:
+        y = y + (np.asarray(X, dtype=F64) @ np.asarray(V, dtype=F64)) @ np.asarray(U, dtype=F64).T
+    return y
+
+
+def qk_norm_rope(x, head_dim, weight, offset, eps, positions, inv_freq, interleaved) -> np.ndarray:
+    """One side of the per-head norm and rotation, in fp64: x [M, heads * head_dim]."""
+    x = np.asarray(x, dtype=F64)
+    M = x.shape[0]
+    h = x.reshape(M, -1, head_dim)
+    h = h / np.sqrt(np.mean(h * h, axis=2, keepdims=True) + F64(np.float32(eps)))
+    if weight is not None:
+        h = h * (np.asarray(weight, dtype=F64) + offset)
+    half = 0 if inv_freq is None else len(inv_freq)
+    y = h.copy()
+    for i in range(half):
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+        t = (np.asarray(positions, dtype=F64) * F64(inv_freq[i]))[:, None]
+        y[:, :, a] = h[:, :, a] * np.cos(t) - h[:, :, b] * np.sin(t)
+        y[:, :, b] = h[:, :, b] * np.cos(t) + h[:, :, a] * np.sin(t)
+    return y.reshape(M, -1)
+
+
 def reconstruct(s, W0, U, V, out_dtype: str = "f64") -> np.ndarray:
     """reconstruct_weight(s, W0, U, V) = diag(s)·W0 + U·Vᵀ
     ("The theta bundle" -- the approximation formula and Key layout)."""
