@@ -11,8 +11,6 @@
 // x * 2^-e rounded to nearest even; a value that is not finite becomes the
 // NaN code and does not count for the scale, so it stays visible in every
 // result it enters instead of turning into 448 * 2^e.
-#include <cuda_fp16.h>
-
 #include <algorithm>
 
 #include "common.cuh"
@@ -173,72 +171,6 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_rows_kernel(const T* __
   }
 }
 
-// ------------------------------------------------------------ forward
-// Y = s (.) (Xq . W0q^T) + T . U^T over 64 x 64 output tiles on CUDA cores, T
-// = X . V in fp32. The simplest form: operands widened to fp32 in shared
-// memory, 128 columns (one block) at a time, each block's sum multiplied by
-// its two scales.
-constexpr int kTile = 64;
-__device__ __forceinline__ float e4m3_to_f32(uint8_t c) {
-  uint32_t h;
-  asm("{.reg .b16 u; cvt.u16.u32 u, %1; cvt.rn.f16x2.e4m3x2 %0, u;}" : "=r"(h) : "r"((uint32_t)c));
-  return __half2float(__ushort_as_half((unsigned short)h));
-}
-
-__global__ void __launch_bounds__(kThreads)
-fp8_forward_simple_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ xs,
-                          const uint8_t* __restrict__ wq, const uint8_t* __restrict__ ws, const float* __restrict__ s,
-                          const bf16* __restrict__ U, const float* __restrict__ T, int64_t M, int64_t O, int64_t I,
-                          int r, bf16* __restrict__ Y) {
-  __shared__ float sx[32][kTile + 1], sw[32][kTile + 1];
-  pdl_enter(xq, xs, wq, ws, s, U, T);
-  const int64_t m0 = (int64_t)blockIdx.y * kTile, o0 = (int64_t)blockIdx.x * kTile;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  float acc[4][4] = {}, part[4][4] = {};
-  const int64_t nb = ceil_div(I, kBlock);
-  for (int64_t b = 0; b < nb; ++b) {
-    for (int k0 = 0; k0 < kBlock; k0 += 32) {
-      __syncthreads();
-      for (int q = threadIdx.x; q < 32 * kTile; q += kThreads) {
-        const int k = q % 32, i = q / 32;
-        const int64_t kk = b * kBlock + k0 + k;
-        sx[k][i] = (kk < I && m0 + i < M) ? e4m3_to_f32(xq[(m0 + i) * I + kk]) : 0.f;
-        sw[k][i] = (kk < I && o0 + i < O) ? e4m3_to_f32(wq[(o0 + i) * I + kk]) : 0.f;
-      }
-      __syncthreads();
-      for (int k = 0; k < 32; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) part[i][j] = fmaf(sx[k][ty * 4 + i], sw[k][tx * 4 + j], part[i][j]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t m = m0 + ty * 4 + i;
-      const int ex = m < M ? (int)xs[b * M + m] - 127 : 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t o = o0 + tx * 4 + j;
-        const int ew = o < O ? (int)ws[o / kBlock * nb + b] - 127 : 0;
-        acc[i][j] += ldexpf(part[i][j], ex + ew);
-        part[i][j] = 0.f;
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = m0 + ty * 4 + i;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t o = o0 + tx * 4 + j;
-      if (m >= M || o >= O) continue;
-      float t = 0.f;
-      for (int q = 0; q < r; ++q) t = fmaf(T[m * r + q], __bfloat162float(U[o * r + q]), t);
-      Y[m * O + o] = __float2bfloat16_rn(fmaf(s[o], acc[i][j], t));
-    }
-  }
-}
-
 }  // namespace
 
 cudaError_t launch_fp8_quantize(const LaunchCtx& c, theta_dtype dt, const void* W, int64_t O, int64_t I, void* codes,
@@ -264,21 +196,12 @@ cudaError_t launch_fp8_quantize_rows(const LaunchCtx& c, theta_dtype dt, const v
                                        static_cast<const float*>(X), M, I, q, e);
 }
 
-size_t forward_fp8_workspace_bytes(int64_t M, int r) { return r > 0 ? (size_t)M * r * sizeof(float) : 0; }
+size_t forward_fp8_workspace_bytes(int64_t M, int r) { return forward_fp8_umma_workspace_bytes(M, r); }
 
 int launch_forward_fp8(const LaunchCtx& c, const void* X, const void* xq, const void* xs, const void* wq,
                        const void* ws, const float* s, const void* U, const void* V, int64_t M, int64_t O, int64_t I,
                        int r, void* Y, void* work, cudaError_t* ce) {
-  *ce = cudaSuccess;
-  if (M > kSimtMaxRows || ceil_div(O, kTile) > INT32_MAX) return THETA_ERR_UNSUPPORTED;
-  float* T = static_cast<float*>(work);
-  if (r > 0) *ce = launch_xv_simt(c, THETA_BF16, X, V, M, I, r, T);
-  if (*ce == cudaSuccess)
-    *ce = launch_pdl(fp8_forward_simple_kernel, dim3((unsigned)ceil_div(O, kTile), (unsigned)ceil_div(M, kTile)),
-                     dim3(kThreads), 0, c.stream, 1, static_cast<const uint8_t*>(xq), static_cast<const uint8_t*>(xs),
-                     static_cast<const uint8_t*>(wq), static_cast<const uint8_t*>(ws), s,
-                     static_cast<const bf16*>(U), (const float*)T, M, O, I, r, static_cast<bf16*>(Y));
-  return *ce == cudaSuccess ? THETA_OK : THETA_ERR_CUDA;
+  return launch_forward_fp8_umma(c, X, xq, xs, wq, ws, s, U, V, M, O, I, r, Y, work, ce);
 }
 
 }  // namespace theta

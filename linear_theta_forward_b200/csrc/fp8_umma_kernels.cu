@@ -1,0 +1,688 @@
+// The block-scaled FP8 theta forward on tensor cores (sm_100a):
+//   Y[m, o] = s[o] * D1[o, m] + D2[o, m]
+//   D1 = sum over blocks b of 128 columns of 2^(ew + ex) Wq[o, b] . Xq[m, b]
+//   D2 = U . (T_hi + T_lo)^T,  T = X . V
+// D1 runs on kind::mxf8f6f4: E4M3 operands, and for each row of A and of B a
+// power-of-two scale per 32 values of K that the tensor core applies itself.
+// Here all four 32-wide steps of a 128-wide K block use one scale, so a word
+// of four scale bytes in tensor memory serves four K blocks (512 columns): a
+// "scale group", selected byte by byte in the instruction descriptor. D2 is
+// the bf16 rank term of the bf16 forward, in its own accumulator.
+//
+// As in the bf16 forward, W0 rows are the MMA's M side (128 rows are exactly
+// one block of scales, so a tile's A scales are one byte per K block), tokens
+// its N side, and s is a per-thread factor in the epilogue.
+//
+// Roles of a CTA's warps:
+//   warp 0       TMA producer (one lane): 128 x 128 bytes of W0 codes and the
+//                tile's token codes per stage, 128-byte swizzle
+//   warp 1       tensor-memory allocation; MMA issuer (one lane)
+//   warps 2-5    the scales: bytes from global memory, packed in registers and
+//                written to tensor memory (tcgen05.st), each warp its 32-lane
+//                quarter, a ring of groups ahead of the MMAs
+//   epilogue     the same warps 2-5 after the last group (one-SM tiles); warps
+//                6-13 of their own in the persistent CTA-pair kernel
+// Waits are bounded as everywhere in the library.
+#include <cuda.h>
+
+#include <mutex>
+
+#include "common.cuh"
+#include "internal.h"
+#include "umma_host.cuh"
+#include "umma_ptx.cuh"
+
+namespace theta {
+
+namespace {
+
+constexpr int kBM = 128;
+constexpr int kBK = 128;               // bytes of K per stage: 128 codes, or 64 bf16 of the rank term
+constexpr int kRankBK = 64;
+constexpr int kABytes = kBM * 128;
+constexpr int kGroup = 4;              // K blocks per scale word
+constexpr int kPitch = 129;            // fp32 pitch of the split-K partial tiles
+constexpr uint32_t kOne = 0x7f7f7f7fu;  // four scales of 1
+
+struct Args {
+  int rows;   // O
+  int cols;   // M tokens
+  int kb1;    // K blocks of 128 codes
+  int kb2;    // rank blocks of 64 (0: none)
+  int splits;
+  const uint8_t* xs;  // [kb1, cols]
+  const uint8_t* ws;  // [ceil(rows / 128), kb1]
+  const float* s;
+  bf16* out;
+  int early_start;  // launched right after this call's T = X.V kernel
+  unsigned* err;
+};
+
+// The scale words of K blocks [kb, kb + 4) below kb_end: bytes at p + j * pitch.
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* p, int64_t pitch, int kb, int kb_end) {
+  uint32_t w = kOne;
+#pragma unroll
+  for (int j = 0; j < kGroup; ++j)
+    if (kb + j < kb_end) w = (w & ~(0xffu << (8 * j))) | ((uint32_t)p[(int64_t)(kb + j) * pitch] << (8 * j));
+  return w;
+}
+
+// ------------------------------------------------------------ one-SM tiles
+constexpr int kThreads = 192;
+
+template <int BN>
+struct Cfg {
+  static constexpr int kBBytes = BN * 128;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = 4;
+  static constexpr int kRing = 4;                          // scale groups in tensor memory
+  static constexpr int kSfbCols = BN <= 32 ? 1 : BN / 32;  // columns of token scales
+  static constexpr int kSf = 2 * BN;                       // first scale column (after D1, D2); 8 per group
+  static constexpr int kTmemNeed = kSf + 8 * kRing;
+  static constexpr int kTmemCols = kTmemNeed <= 64 ? 64 : kTmemNeed <= 128 ? 128 : kTmemNeed <= 256 ? 256 : 512;
+  static_assert(kTmemNeed <= 512 && kSfbCols <= 4, "accumulators and scales must fit in tensor memory");
+  static_assert(BN * kPitch * 4 <= kStages * kStageBytes, "partial tile must fit in the stage ring");
+  static constexpr int kSmemBytes = kStages * kStageBytes + 1024 /*align*/ + 256 /*barriers*/;
+};
+
+template <int BN>
+__global__ void __launch_bounds__(kThreads)
+fp8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmTh,
+                const __grid_constant__ CUtensorMap tmTl, const __grid_constant__ Args args) {
+  using C = Cfg<BN>;
+  constexpr int S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * C::kStageBytes);
+  uint64_t* empty = full + S;
+  uint64_t* sf_full = empty + S;
+  uint64_t* sf_empty = sf_full + C::kRing;
+  uint64_t* accum = sf_empty + C::kRing;
+  uint64_t* drain = accum + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int split = args.splits > 1 ? (int)ptx::cluster_ctarank() : 0;
+  const int n_tile = blockIdx.x / args.splits;
+  const int m_tile = blockIdx.y;
+  const int kb_begin = (int)((int64_t)split * args.kb1 / args.splits);
+  const int kb_end = (int)((int64_t)(split + 1) * args.kb1 / args.splits);
+  const bool has_d2 = args.kb2 > 0 && split == 0;
+  const int n1 = kb_end - kb_begin;
+  const int total = n1 + (has_d2 ? 2 * args.kb2 : 0);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      ptx::mbar_init(&full[i], 1);
+      ptx::mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < C::kRing; ++i) {
+      ptx::mbar_init(&sf_full[i], 4);  // one arrival per scale warp
+      ptx::mbar_init(&sf_empty[i], 1);
+    }
+    ptx::mbar_init(accum, 1);
+    ptx::mbar_init(drain, 1);
+    *abort_flag = prior_timeout(args.err);
+    ptx::fence_mbarrier_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(tmem_slot, C::kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // programmatic dependent launch as in the bf16 forward: right after its own
+  // T = X.V kernel (which has seen all earlier work complete) the codes,
+  // scales and s are streamed at once, and only the loads of T wait
+  const bool early = args.early_start;
+  if (!early) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  auto give_up = [&]() {
+    record_timeout(args.err);
+    *abort_flag = 1;
+  };
+
+  if (warp == 0 && lane == 0) {
+    // ---------------------------------------------------------- producer
+    ptx::prefetch_tmap(&tmW);
+    ptx::prefetch_tmap(&tmX);
+    int issued = 0;
+    for (int i = 0; i < total; ++i) {
+      const int st = i % S;
+      if (!ptx::mbar_wait(&empty[st], ((uint32_t)(i / S) & 1u) ^ 1u, abort_flag)) {
+        give_up();
+        break;
+      }
+      uint8_t* a = smem + st * C::kStageBytes;
+      uint8_t* b = a + kABytes;
+      ptx::mbar_arrive_expect_tx(&full[st], C::kStageBytes);
+      if (i < n1) {
+        ptx::tma_load_2d(a, &tmW, &full[st], (kb_begin + i) * kBK, m_tile * kBM);
+        ptx::tma_load_2d(b, &tmX, &full[st], (kb_begin + i) * kBK, n_tile * BN);
+      } else {
+        const int j = i - n1;
+        if (early && j == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+        const int jx = (j % args.kb2) * kRankBK;
+        ptx::tma_load_2d(a, &tmU, &full[st], jx, m_tile * kBM);
+        ptx::tma_load_2d(b, j < args.kb2 ? &tmTh : &tmTl, &full[st], jx, n_tile * BN);
+      }
+      ++issued;
+    }
+    // drain: wait for the last armed phase of every stage (all loads landed)
+    for (int st = 0; st < S && st < issued; ++st) {
+      const int last = st + ((issued - 1 - st) / S) * S;
+      if (!ptx::mbar_wait(&full[st], (uint32_t)(last / S) & 1u, abort_flag)) {
+        int never = 0;
+        ptx::mbar_wait(&full[st], (uint32_t)(last / S) & 1u, &never);
+      }
+    }
+  } else if (warp == 1 && lane == 0) {
+    // ---------------------------------------------------------- MMA issuer
+    int done = 0;
+    for (int i = 0; i < total; ++i) {
+      const int st = i % S, g = i / kGroup, ring = g % C::kRing;
+      bool ok = ptx::mbar_wait(&full[st], (uint32_t)(i / S) & 1u, abort_flag);
+      if (ok && i < n1 && i % kGroup == 0)
+        ok = ptx::mbar_wait(&sf_full[ring], (uint32_t)(g / C::kRing) & 1u, abort_flag);
+      if (!ok) {
+        give_up();
+        break;
+      }
+      ptx::tc_fence_after();
+      const uint32_t a = ptx::smem_u32(smem + st * C::kStageBytes);
+      const uint32_t b = a + kABytes;
+      if (i < n1) {
+        const uint32_t sf = tmem + (uint32_t)(C::kSf + 8 * ring);
+        const uint32_t idesc = ptx::idesc_mxf8(kBM, BN, i % kGroup);
+#pragma unroll
+        for (int kk = 0; kk < kBK / 32; ++kk)
+          ptx::umma_mxf8<false>(tmem, ptx::sdesc_sw128(a + kk * 32, 16, 1024), ptx::sdesc_sw128(b + kk * 32, 16, 1024),
+                                idesc, sf, sf + 4, (i > 0 || kk > 0) ? 1u : 0u);
+        if (i % kGroup == kGroup - 1) ptx::umma_commit(&sf_empty[ring]);
+      } else {
+        constexpr uint32_t idesc = ptx::idesc_bf16(kBM, BN, 0);
+#pragma unroll
+        for (int kk = 0; kk < kRankBK / 16; ++kk)
+          ptx::umma_bf16(tmem + BN, ptx::sdesc_sw128(a + kk * 32, 16, 1024), ptx::sdesc_sw128(b + kk * 32, 16, 1024),
+                         idesc, (i > n1 || kk > 0) ? 1u : 0u);
+      }
+      ptx::umma_commit(&empty[st]);
+      ++done;
+    }
+    if (done == total) {
+      ptx::umma_commit(accum);
+    } else if (done > 0) {
+      // aborted: the issued MMAs finish before tensor memory is freed
+      ptx::umma_commit(drain);
+      int never = 0;
+      ptx::mbar_wait(drain, 0, &never);
+    }
+  } else if (warp >= 2) {
+    // ---------------------------------------------------------- scales
+    const int quarter = warp & 3;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint8_t* wsp = args.ws + (int64_t)m_tile * args.kb1;
+    const int groups = (n1 + kGroup - 1) / kGroup;
+    for (int g = 0; g < groups; ++g) {
+      const int ring = g % C::kRing, kb = kb_begin + g * kGroup;
+      const uint32_t wa = scale_word(wsp, 1, kb, kb_end);
+      uint32_t wb[C::kSfbCols];
+#pragma unroll
+      for (int c = 0; c < C::kSfbCols; ++c) {
+        const int m = n_tile * BN + 32 * c + lane;
+        wb[c] = m < args.cols && 32 * c + lane < BN ? scale_word(args.xs + m, args.cols, kb, kb_end) : kOne;
+      }
+      bool ok = g < C::kRing || ptx::mbar_wait(&sf_empty[ring], (uint32_t)(g / C::kRing - 1) & 1u, abort_flag);
+      if (!ok) give_up();
+      if (!__all_sync(0xffffffffu, ok)) break;
+      ptx::tc_fence_after();
+      const uint32_t sf = tmem + lanes + (uint32_t)(C::kSf + 8 * ring);
+      ptx::tmem_st4(sf, wa, wa, wa, wa);
+      if constexpr (C::kSfbCols == 4) {
+        ptx::tmem_st4(sf + 4, wb[0], wb[1], wb[2], wb[3]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < C::kSfbCols; ++c) ptx::tmem_st1(sf + 4 + c, wb[c]);
+      }
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sf_full[ring]);
+    }
+    // ---------------------------------------------------------- epilogue
+    const int row = quarter * 32 + lane;  // accumulator row = tensor-memory lane
+    const uint32_t taddr = tmem + lanes;
+    if (early) asm volatile("griddepcontrol.wait;" ::: "memory");
+    bool ok = ptx::mbar_wait(accum, 0, abort_flag);
+    if (!ok) give_up();
+    ok = __all_sync(0xffffffffu, ok);  // tcgen05.ld below is warp-collective
+    ptx::tc_fence_after();
+    const int grow = m_tile * kBM + row;
+    const int col0 = n_tile * BN;
+    const int ncols = min(BN, args.cols - col0);
+    const float so = grow < args.rows ? __ldg(args.s + grow) : 0.f;
+    float* part = reinterpret_cast<float*>(smem);
+    if (ok) {
+      for (int c0 = 0; c0 < ncols; c0 += 16) {
+        float d1[16], d2[16];
+        ptx::tmem_ld16(taddr + c0, d1);
+        if (has_d2) ptx::tmem_ld16(taddr + BN + c0, d2);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float v = has_d2 ? fmaf(so, d1[e], d2[e]) : so * d1[e];
+          const int m = col0 + c0 + e;
+          if (args.splits > 1)
+            part[(c0 + e) * kPitch + row] = v;
+          else if (grow < args.rows && m < args.cols)
+            args.out[(int64_t)m * args.rows + grow] = __float2bfloat16_rn(v);
+        }
+      }
+    }
+  }
+
+  // ------------------------------------------------------------ split-K sum
+  __syncwarp();
+  if (args.splits > 1) {
+    ptx::cluster_sync();  // every CTA of the cluster has staged its partial tile
+    if (!*abort_flag) {
+      const int col0 = n_tile * BN;
+      const int E = min(BN, args.cols - col0) * kBM;
+      const int e0 = (int)((int64_t)split * E / args.splits), e1 = (int)((int64_t)(split + 1) * E / args.splits);
+      const uint32_t part_addr = ptx::smem_u32(smem);
+      for (int e = e0 + threadIdx.x; e < e1; e += kThreads) {
+        const int c = e / kBM, rr = e % kBM;
+        const uint32_t off = part_addr + (uint32_t)((c * kPitch + rr) * 4);
+        float v = 0.f;
+        for (int p = 0; p < args.splits; ++p) v += ptx::ld_dsmem_f32(ptx::mapa(off, (uint32_t)p));
+        const int grow = m_tile * kBM + rr;
+        if (grow < args.rows) args.out[(int64_t)(col0 + c) * args.rows + grow] = __float2bfloat16_rn(v);
+      }
+    }
+    ptx::cluster_sync();  // no CTA leaves while a peer still reads its tile
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) ptx::tmem_dealloc(tmem, C::kTmemCols);
+}
+
+// ------------------------------------------------------------ CTA-pair tiles
+// 256 rows x up to 240 tokens per pair of SMs (cta_group::2), persistent. Each
+// CTA stages 128 rows of W0 codes and half of the tile's tokens per K block
+// and holds its 128 rows of both accumulators. 240 tokens, not 256: D1 and D2
+// take 2 x 240 columns of tensor memory and the scales of two groups the
+// other 32. A's scales are each CTA's own rows', B's those of all the tile's
+// tokens, in both CTAs.
+constexpr int kPairN = 240;
+constexpr int kPairHalf = kPairN / 2;
+constexpr int kPairStages = 5;
+constexpr int kPairBBytes = kPairHalf * 128;
+constexpr int kPairStageBytes = kABytes + kPairBBytes;
+constexpr int kPairOutBytes = kBM * kPairN * 2;
+constexpr int kPairSmemBytes = kPairStages * kPairStageBytes + kPairOutBytes + 1024 /*align*/ + 256 /*barriers*/;
+constexpr int kPairSf = 2 * kPairN;  // scale columns: 16 per group, two groups
+constexpr int kPairRing = 2;
+constexpr int kPairEpiWarps = 8;
+constexpr int kPairEpi = 32 * kPairEpiWarps;
+constexpr int kPairThreads = 64 + 128 + kPairEpi;
+constexpr uint16_t kPairMask = 0x3;
+static_assert(kPairSf + 16 * kPairRing <= 512, "accumulators and scales must fit in tensor memory");
+static_assert(kPairBBytes % 1024 == 0, "swizzled tiles start on 1024-byte boundaries");
+
+__global__ void __launch_bounds__(kPairThreads, 1)
+fp8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmTh,
+                const __grid_constant__ CUtensorMap tmTl, const __grid_constant__ CUtensorMap tmY,
+                const __grid_constant__ Args args) {
+  constexpr int S = kPairStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  bf16* sOut = reinterpret_cast<bf16*>(smem + S * kPairStageBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * kPairStageBytes + kPairOutBytes);
+  uint64_t* empty = full + S;
+  uint64_t* sf_full = empty + S;
+  uint64_t* sf_empty = sf_full + kPairRing;
+  uint64_t* accum = sf_empty + kPairRing;
+  uint64_t* tmem_free = accum + 1;
+  uint64_t* drain = tmem_free + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t cta = ptx::cluster_ctarank();  // 0 issues the MMAs
+  const int cluster = blockIdx.x / 2, n_clusters = gridDim.x / 2;
+  const int n_tiles = (args.cols + kPairN - 1) / kPairN;
+  const int tiles = n_tiles * ((args.rows + 2 * kBM - 1) / (2 * kBM));
+  const bool has_d2 = args.kb2 > 0;
+  const int n1 = args.kb1;
+  const int per_tile = n1 + (has_d2 ? 2 * args.kb2 : 0);
+  const int groups = (n1 + kGroup - 1) / kGroup;
+  // tokens of a tile's MMA: the last tile's rounded up to a multiple of 16
+  auto tile_n = [&](int tile) { return min(kPairN, (args.cols - (tile % n_tiles) * kPairN + 15) / 16 * 16); };
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      ptx::mbar_init(&full[i], 1);
+      ptx::mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < kPairRing; ++i) {
+      ptx::mbar_init(&sf_full[i], 8);  // one arrival per scale warp of both CTAs
+      ptx::mbar_init(&sf_empty[i], 1);
+    }
+    ptx::mbar_init(accum, 1);
+    ptx::mbar_init(tmem_free, 2 * kPairEpiWarps);  // one arrival per epilogue warp of both CTAs
+    ptx::mbar_init(drain, 1);
+    *abort_flag = prior_timeout(args.err);
+    ptx::fence_mbarrier_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(tmem_slot, 512);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  ptx::cluster_sync();  // both CTAs' barriers exist before either signals the other's
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const bool early = args.early_start;
+  if (!early) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  auto give_up = [&]() {
+    record_timeout(args.err);
+    *abort_flag = 1;
+  };
+
+  if (warp == 0 && lane == 0) {
+    // ---------------------------------------------------------- producer (both CTAs)
+    ptx::prefetch_tmap(&tmW);
+    ptx::prefetch_tmap(&tmX);
+    const uint32_t full0 = ptx::mapa(ptx::smem_u32(full), 0);  // the MMA CTA's full barriers
+    bool waited = !early, stop = false;
+    int g = 0;  // stage items issued, over all tiles
+    for (int tile = cluster; tile < tiles && !stop; tile += n_clusters) {
+      const int row0 = (tile / n_tiles) * (2 * kBM) + (int)cta * kBM;
+      const int tok0 = (tile % n_tiles) * kPairN + (int)cta * (tile_n(tile) / 2);
+      for (int i = 0; i < per_tile; ++i, ++g) {
+        const int st = g % S;
+        if (!ptx::mbar_wait(&empty[st], ((uint32_t)(g / S) & 1u) ^ 1u, abort_flag)) {
+          give_up();
+          stop = true;
+          break;
+        }
+        uint8_t* a = smem + st * kPairStageBytes;
+        uint8_t* b = a + kABytes;
+        const uint32_t bar = full0 + (uint32_t)(st * 8);
+        if (cta == 0) ptx::mbar_arrive_expect_tx(&full[st], 2 * kPairStageBytes);  // both CTAs' loads
+        if (i < n1) {
+          ptx::tma_load_2d_pair(a, &tmW, bar, i * kBK, row0);
+          ptx::tma_load_2d_pair(b, &tmX, bar, i * kBK, tok0);
+        } else {
+          const int j = i - n1;
+          if (!waited) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            waited = true;
+          }
+          const int jx = (j % args.kb2) * kRankBK;
+          ptx::tma_load_2d_pair(a, &tmU, bar, jx, row0);
+          ptx::tma_load_2d_pair(b, j < args.kb2 ? &tmTh : &tmTl, bar, jx, tok0);
+        }
+      }
+    }
+    // drain: a stage's last MMAs complete after its last loads landed, and
+    // their commit reaches empty[] in both CTAs. After an abort, loads in
+    // flight land within microseconds: a bounded tenth of a second for them
+    for (int st = 0; st < S && st < g; ++st) {
+      const int last = st + ((g - 1 - st) / S) * S;
+      if (!ptx::mbar_wait(&empty[st], (uint32_t)(last / S) & 1u, abort_flag)) {
+        int never = 0;
+        ptx::mbar_wait(&empty[st], (uint32_t)(last / S) & 1u, &never, 100000000ull);
+      }
+    }
+  } else if (warp == 1 && lane == 0 && cta == 0) {
+    // ---------------------------------------------------------- MMA issuer (even CTA)
+    bool stop = false;
+    int g = 0, j = 0, sg = 0, issued = 0;  // stage items, tiles, scale groups
+    for (int tile = cluster; tile < tiles; tile += n_clusters, ++j) {
+      // the epilogues of both CTAs have read the previous tile's accumulators
+      if (j > 0 && !ptx::mbar_wait(tmem_free, (uint32_t)(j - 1) & 1u, abort_flag)) {
+        give_up();
+        stop = true;
+        break;
+      }
+      ptx::tc_fence_after();
+      const int N = tile_n(tile);
+      for (int i = 0; i < per_tile; ++i, ++g) {
+        const int st = g % S, ring = sg % kPairRing;
+        bool ok = ptx::mbar_wait(&full[st], (uint32_t)(g / S) & 1u, abort_flag);
+        if (ok && i < n1 && i % kGroup == 0)
+          ok = ptx::mbar_wait(&sf_full[ring], (uint32_t)(sg / kPairRing) & 1u, abort_flag);
+        if (!ok) {
+          give_up();
+          stop = true;
+          break;
+        }
+        ptx::tc_fence_after();
+        const uint32_t a = ptx::smem_u32(smem + st * kPairStageBytes);
+        const uint32_t b = a + kABytes;
+        if (i < n1) {
+          const uint32_t sf = tmem + (uint32_t)(kPairSf + 16 * ring);
+          const uint32_t idesc = ptx::idesc_mxf8(2 * kBM, N, i % kGroup);
+#pragma unroll
+          for (int kk = 0; kk < kBK / 32; ++kk)
+            ptx::umma_mxf8<true>(tmem, ptx::sdesc_sw128(a + kk * 32, 16, 1024), ptx::sdesc_sw128(b + kk * 32, 16, 1024),
+                                 idesc, sf, sf + 4, (i > 0 || kk > 0) ? 1u : 0u);
+          if (i % kGroup == kGroup - 1 || i == n1 - 1) {
+            ptx::umma_commit_pair(&sf_empty[ring], kPairMask);
+            ++sg;
+          }
+        } else {
+          const uint32_t idesc = ptx::idesc_bf16(2 * kBM, N, 0);
+#pragma unroll
+          for (int kk = 0; kk < kRankBK / 16; ++kk)
+            ptx::umma_bf16_pair(tmem + (uint32_t)kPairN, ptx::sdesc_sw128(a + kk * 32, 16, 1024),
+                                ptx::sdesc_sw128(b + kk * 32, 16, 1024), idesc, (i > n1 || kk > 0) ? 1u : 0u);
+        }
+        ptx::umma_commit_pair(&empty[st], kPairMask);
+        ++issued;
+      }
+      if (stop) break;
+      ptx::umma_commit_pair(accum, kPairMask);
+    }
+    if (stop && issued > 0) {
+      // aborted: the issued MMAs finish before tensor memory is released
+      ptx::umma_commit_pair(drain, 0x1);
+      int never = 0;
+      ptx::mbar_wait(drain, 0, &never);
+    }
+  } else if (warp >= 2 && warp < 6) {
+    // ---------------------------------------------------------- scales (both CTAs)
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t full_bar = ptx::mapa(ptx::smem_u32(sf_full), 0);
+    const int row_blocks = (args.rows + kBM - 1) / kBM;
+    bool ok = true;
+    int sg = 0;
+    for (int tile = cluster; tile < tiles && ok; tile += n_clusters) {
+      // the odd CTA's rows may all be past O: its scales are then not used
+      const int rb = min((tile / n_tiles) * 2 + (int)cta, row_blocks - 1);
+      const uint8_t* wsp = args.ws + (int64_t)rb * args.kb1;
+      const int tok = (tile % n_tiles) * kPairN + lane;
+      for (int q = 0; q < groups; ++q, ++sg) {
+        const int ring = sg % kPairRing, kb = q * kGroup;
+        const uint32_t wa = scale_word(wsp, 1, kb, n1);
+        uint32_t wb[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const int m = tok + 32 * c;
+          wb[c] = m < args.cols ? scale_word(args.xs + m, args.cols, kb, n1) : kOne;
+        }
+        ok = sg < kPairRing || ptx::mbar_wait(&sf_empty[ring], (uint32_t)(sg / kPairRing - 1) & 1u, abort_flag);
+        if (!ok) give_up();
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t sf = tmem + lanes + (uint32_t)(kPairSf + 16 * ring);
+        ptx::tmem_st4(sf, wa, wa, wa, wa);
+        ptx::tmem_st4(sf + 4, wb[0], wb[1], wb[2], wb[3]);
+        ptx::tmem_st4(sf + 8, wb[4], wb[5], wb[6], wb[7]);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(full_bar + (uint32_t)(ring * 8));
+      }
+    }
+  } else if (warp >= 6) {
+    // ---------------------------------------------------------- epilogue (both CTAs)
+    const int quarter = warp & 3;         // a warp reads lanes 32 * (warp % 4) ...
+    const int part = (warp - 6) / 4;      // ... and columns [128 * part, ...)
+    const int row = quarter * 32 + lane;  // accumulator row = tensor-memory lane
+    const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16);
+    const bool storer = threadIdx.x == 192;  // issues the TMA stores of the tile
+    const uint32_t free_bar = ptx::mapa(ptx::smem_u32(tmem_free), 0);
+    if (early) asm volatile("griddepcontrol.wait;" ::: "memory");
+    bool ok = true;
+    int j = 0;
+    for (int tile = cluster; tile < tiles; tile += n_clusters, ++j) {
+      const int row0 = (tile / n_tiles) * (2 * kBM) + (int)cta * kBM;
+      const int col0 = (tile % n_tiles) * kPairN;
+      const int ncols = min(kPairN, args.cols - col0);
+      if (storer) ptx::bulk_wait_read();  // the previous tile's store has read sOut
+      const bool got = ptx::mbar_wait(accum, (uint32_t)j & 1u, abort_flag);
+      // one decision for all epilogue warps: the barriers below need every one of them
+      ok = ptx::bar_red_and(1, kPairEpi, got);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      const int grow = row0 + row;
+      const float so = grow < args.rows ? __ldg(args.s + grow) : 0.f;
+      const int c_end = min(ncols, part * 128 + 128);
+      for (int c0 = part * 128; c0 < c_end; c0 += 16) {
+        float d1[16], d2[16];
+        ptx::tmem_ld16(taddr + c0, d1);
+        if (has_d2) ptx::tmem_ld16(taddr + kPairN + c0, d2);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          sOut[(c0 + e) * kBM + row] = __float2bfloat16_rn(has_d2 ? fmaf(so, d1[e], d2[e]) : so * d1[e]);
+      }
+      // tensor memory read: the next tile's MMAs may start
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(free_bar);
+      ptx::fence_proxy_async_smem();
+      asm volatile("bar.sync 1, %0;" ::"n"(kPairEpi) : "memory");
+      if (storer && row0 < args.rows) {
+        // rows past O and tokens past M fall outside Y and are not written
+        ptx::tma_store_2d(&tmY, sOut, row0, col0);
+        ptx::bulk_commit();
+      }
+    }
+    if (!ok && !*abort_flag) give_up();
+    if (storer) ptx::bulk_wait_all();
+  }
+
+  __syncwarp();
+  ptx::tc_fence_before();
+  ptx::cluster_sync();  // both epilogues have read their accumulators; every MMA has completed
+  if (warp == 1) ptx::tmem_dealloc_pair(tmem, 512);
+}
+
+// ------------------------------------------------------------------ host side
+struct Maps {
+  CUtensorMap w, x, u, th, tl;
+};
+
+template <int BN>
+cudaError_t launch_tile(const LaunchCtx& c, const Maps& mp, Args args) {
+  using C = Cfg<BN>;
+  auto kern = fp8_tile_kernel<BN>;
+  static KernelInfo info[64];
+  cudaError_t e = prepare_kernel(&info[c.device], c.device, kern, kThreads, C::kSmemBytes, C::kTmemCols, true);
+  if (e != cudaSuccess) return e;
+  const int m_tiles = (int)ceil_div(args.rows, kBM), n_tiles = (int)ceil_div(args.cols, BN);
+  // as in the bf16 forward: tiles of 64 or more tokens count one CTA per SM
+  const int capacity = c.num_sms * (BN >= 64 ? 1 : info[c.device].blocks_per_sm);
+  args.splits = c.policy == THETA_POLICY_THROUGHPUT
+                    ? 1
+                    : pick_splits((int64_t)m_tiles * n_tiles, args.kb1, capacity, info[c.device].max_cluster);
+  return launch_pdl(kern, dim3((unsigned)(n_tiles * args.splits), (unsigned)m_tiles), dim3(kThreads), C::kSmemBytes,
+                    c.stream, args.splits, mp.w, mp.x, mp.u, mp.th, mp.tl, args);
+}
+
+cudaError_t launch_pair(const LaunchCtx& c, const Maps& mp, const Args& args, const CUtensorMap& mY) {
+  static KernelInfo info[64];
+  cudaError_t e =
+      prepare_kernel(&info[c.device], c.device, fp8_pair_kernel, kPairThreads, kPairSmemBytes, 512, false);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = ceil_div(args.rows, 2 * kBM) * ceil_div(args.cols, kPairN);
+  const int64_t clusters = tiles < c.num_sms / 2 ? tiles : c.num_sms / 2;  // one CTA per SM
+  return launch_pdl(fp8_pair_kernel, dim3((unsigned)(2 * clusters)), dim3(kPairThreads), kPairSmemBytes, c.stream, 2,
+                    mp.w, mp.x, mp.u, mp.th, mp.tl, mY, args);
+}
+
+}  // namespace
+
+size_t forward_fp8_umma_workspace_bytes(int64_t M, int r) {
+  const size_t half = ((size_t)M * r * 2 + 255) / 256 * 256;
+  return 2 * half;  // T's high and low parts
+}
+
+int launch_forward_fp8_umma(const LaunchCtx& c, const void* X, const void* xq, const void* xs, const void* wq,
+                            const void* ws, const float* s, const void* U, const void* V, int64_t M, int64_t O,
+                            int64_t I, int r, void* Y, void* work, cudaError_t* ce) {
+  *ce = cudaSuccess;
+  int st;
+  bf16* t_hi = static_cast<bf16*>(work);
+  bf16* t_lo = nullptr;
+  if (r > 0) {
+    t_lo = reinterpret_cast<bf16*>(static_cast<uint8_t*>(work) + forward_fp8_umma_workspace_bytes(M, r) / 2);
+    if ((st = launch_xv_umma(c, X, V, M, I, r, t_hi, t_lo, ce))) return st;
+  }
+  const int m_tiles = (int)ceil_div(O, kBM);
+  // Pairs when they fill the GPU, or when every CTA takes a whole tile anyway
+  const bool pair =
+      M > 128 && (c.policy == THETA_POLICY_THROUGHPUT || m_tiles * ceil_div(M, kPairN) >= (int64_t)c.num_sms);
+  const int BN = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  const int box = pair ? kPairHalf : BN;  // tokens per box
+  Maps mp;
+  if ((st = make_map_box(&mp.w, wq, O, I, kBM, kBK, CU_TENSOR_MAP_SWIZZLE_128B, ce, 1))) return st;
+  if ((st = make_map_box(&mp.x, xq, M, I, box, kBK, CU_TENSOR_MAP_SWIZZLE_128B, ce, 1))) return st;
+  mp.u = mp.w;
+  mp.th = mp.tl = mp.x;
+  if (r > 0) {
+    if ((st = make_map_box(&mp.u, U, O, r, kBM, kRankBK, CU_TENSOR_MAP_SWIZZLE_128B, ce))) return st;
+    if ((st = make_map_box(&mp.th, t_hi, M, r, box, kRankBK, CU_TENSOR_MAP_SWIZZLE_128B, ce))) return st;
+    if ((st = make_map_box(&mp.tl, t_lo, M, r, box, kRankBK, CU_TENSOR_MAP_SWIZZLE_128B, ce))) return st;
+  }
+  Args a = {};
+  a.rows = (int)O;
+  a.cols = (int)M;
+  a.kb1 = (int)ceil_div(I, kBK);
+  a.kb2 = (int)ceil_div(r, kRankBK);
+  a.splits = 1;
+  a.xs = static_cast<const uint8_t*>(xs);
+  a.ws = static_cast<const uint8_t*>(ws);
+  a.s = s;
+  a.out = static_cast<bf16*>(Y);
+  a.early_start = r > 0;
+  a.err = c.err;
+  if (pair) {
+    CUtensorMap mY;
+    if ((st = make_map_box(&mY, Y, M, O, kPairN, kBM, CU_TENSOR_MAP_SWIZZLE_NONE, ce))) return st;
+    *ce = launch_pair(c, mp, a, mY);
+  } else {
+    switch (BN) {
+      case 16: *ce = launch_tile<16>(c, mp, a); break;
+      case 32: *ce = launch_tile<32>(c, mp, a); break;
+      case 64: *ce = launch_tile<64>(c, mp, a); break;
+      default: *ce = launch_tile<128>(c, mp, a); break;
+    }
+  }
+  return *ce == cudaSuccess ? THETA_OK : THETA_ERR_CUDA;
+}
+
+}  // namespace theta

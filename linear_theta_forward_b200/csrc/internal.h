@@ -1,6 +1,7 @@
 // Internal launcher declarations shared by the libtheta translation units.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -98,6 +99,11 @@ cudaError_t launch_fp8_quantize(const LaunchCtx& c, theta_dtype dt, const void* 
 cudaError_t launch_fp8_quantize_rows(const LaunchCtx& c, theta_dtype dt, const void* X, int64_t M, int64_t I,
                                      void* codes, void* scales);
 size_t forward_fp8_workspace_bytes(int64_t M, int r);
+// The tensor-core forward (fp8_umma_kernels.cu).
+size_t forward_fp8_umma_workspace_bytes(int64_t M, int r);
+int launch_forward_fp8_umma(const LaunchCtx& c, const void* X, const void* xq, const void* xs, const void* wq,
+                            const void* ws, const float* s, const void* U, const void* V, int64_t M, int64_t O,
+                            int64_t I, int r, void* Y, void* work, cudaError_t* ce);
 int launch_forward_fp8(const LaunchCtx& c, const void* X, const void* xq, const void* xs, const void* wq,
                        const void* ws, const float* s, const void* U, const void* V, int64_t M, int64_t O, int64_t I,
                        int r, void* Y, void* work, cudaError_t* ce);
@@ -140,6 +146,10 @@ size_t forward_umma_workspace_bytes(int64_t M, int r);
 int launch_forward_umma(const LaunchCtx& c, const void* X, const void* W0, const float* s,
                         const void* U, const void* V, int64_t M, int64_t O, int64_t I, int r,
                         void* Y, void* ws, cudaError_t* cuda_err);
+// T = X . V (bf16, fp32 accumulation) as bf16 high and low parts [M, r];
+// r <= 256, at most 65535 * 128 tokens.
+int launch_xv_umma(const LaunchCtx& c, const void* X, const void* V, int64_t M, int64_t I, int r, __nv_bfloat16* t_hi,
+                   __nv_bfloat16* t_lo, cudaError_t* ce);
 // One bounded wait that nothing completes (gives up after limit_ms).
 cudaError_t launch_wait_selftest(const LaunchCtx& c, unsigned limit_ms);
 // Fused gate/up: Y = gelu_tanh(gate forward) * (up forward), one tile kernel
