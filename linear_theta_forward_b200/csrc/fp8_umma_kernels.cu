@@ -42,7 +42,6 @@ constexpr int kRankBK = 64;
 constexpr int kABytes = kBM * 128;
 constexpr int kGroup = 4;              // K blocks per scale word
 constexpr int kPitch = 129;            // fp32 pitch of the split-K partial tiles
-constexpr uint32_t kOne = 0x7f7f7f7fu;  // four scales of 1
 
 struct Args {
   int rows;   // O
@@ -58,13 +57,23 @@ struct Args {
   unsigned* err;
 };
 
-// The scale words of K blocks [kb, kb + 4) below kb_end: bytes at p + j * pitch.
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* p, int64_t pitch, int kb, int kb_end) {
-  uint32_t w = kOne;
+// The scale words of N rows for K blocks [kb, kb + 4): bytes at p[row + block *
+// pitch]. Blocks and rows past the end repeat the last one -- their scales
+// meet no MMA, or only columns that are never stored -- so that every load is
+// unconditional and all of them are in flight together.
+template <int N>
+__device__ __forceinline__ void scale_words(const uint8_t* p, int64_t pitch, int row, int last_row, int kb, int last_kb,
+                                            uint32_t (&w)[N]) {
+  uint32_t byte[N][kGroup];
 #pragma unroll
-  for (int j = 0; j < kGroup; ++j)
-    if (kb + j < kb_end) w = (w & ~(0xffu << (8 * j))) | ((uint32_t)p[(int64_t)(kb + j) * pitch] << (8 * j));
-  return w;
+  for (int j = 0; j < kGroup; ++j) {
+    const uint8_t* q = p + (int64_t)min(kb + j, last_kb) * pitch;
+#pragma unroll
+    for (int c = 0; c < N; ++c) byte[c][j] = q[min(row + 32 * c, last_row)];
+  }
+#pragma unroll
+  for (int c = 0; c < N; ++c)
+    w[c] = __byte_perm(byte[c][0] | (byte[c][1] << 8), byte[c][2] | (byte[c][3] << 8), 0x5410);
 }
 
 // ------------------------------------------------------------ one-SM tiles
@@ -103,7 +112,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int split = args.splits > 1 ? (int)ptx::cluster_ctarank() : 0;
   const int n_tile = blockIdx.x / args.splits;
   const int m_tile = blockIdx.y;
@@ -134,7 +143,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   // programmatic dependent launch as in the bf16 forward: right after its own
   // T = X.V kernel (which has seen all earlier work complete) the codes,
   // scales and s are streamed at once, and only the loads of T wait
@@ -181,44 +190,53 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         ptx::mbar_wait(&full[st], (uint32_t)(last / S) & 1u, &never);
       }
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    int done = 0;
+    // The whole warp walks the loop, so that addresses and descriptors stay in
+    // uniform registers, and one lane issues.
+    const bool issuer = ptx::elect_one();
+    const uint64_t desc0 = ptx::sdesc_sw128(ptx::smem_u32(smem), 16, 1024);
+    int done = 0, st = 0, ring = 0;
+    uint32_t ph = 0, ring_ph = 0;
     for (int i = 0; i < total; ++i) {
-      const int st = i % S, g = i / kGroup, ring = g % C::kRing;
-      bool ok = ptx::mbar_wait(&full[st], (uint32_t)(i / S) & 1u, abort_flag);
-      if (ok && i < n1 && i % kGroup == 0)
-        ok = ptx::mbar_wait(&sf_full[ring], (uint32_t)(g / C::kRing) & 1u, abort_flag);
-      if (!ok) {
+      const int byte = i % kGroup;
+      bool ok = ptx::mbar_wait(&full[st], ph, abort_flag);
+      if (ok && i < n1 && byte == 0) ok = ptx::mbar_wait(&sf_full[ring], ring_ph, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) {
         give_up();
         break;
       }
       ptx::tc_fence_after();
-      const uint32_t a = ptx::smem_u32(smem + st * C::kStageBytes);
-      const uint32_t b = a + kABytes;
+      const uint64_t ad = desc0 + (uint64_t)(st * (C::kStageBytes / 16));
+      const uint64_t bd = ad + kABytes / 16;
       if (i < n1) {
         const uint32_t sf = tmem + (uint32_t)(C::kSf + 8 * ring);
-        const uint32_t idesc = ptx::idesc_mxf8(kBM, BN, i % kGroup);
+        const uint32_t idesc = ptx::idesc_mxf8(kBM, BN, byte);
+        if (issuer) {
 #pragma unroll
-        for (int kk = 0; kk < kBK / 32; ++kk)
-          ptx::umma_mxf8<false>(tmem, ptx::sdesc_sw128(a + kk * 32, 16, 1024), ptx::sdesc_sw128(b + kk * 32, 16, 1024),
-                                idesc, sf, sf + 4, (i > 0 || kk > 0) ? 1u : 0u);
-        if (i % kGroup == kGroup - 1) ptx::umma_commit(&sf_empty[ring]);
-      } else {
+          for (int kk = 0; kk < kBK / 32; ++kk)
+            ptx::umma_mxf8<false>(tmem, ad + 2 * kk, bd + 2 * kk, idesc, sf, sf + 4, (i > 0 || kk > 0) ? 1u : 0u);
+          if (byte == kGroup - 1) ptx::umma_commit(&sf_empty[ring]);
+          ptx::umma_commit(&empty[st]);
+        }
+        if (byte == kGroup - 1 && ++ring == C::kRing) ring = 0, ring_ph ^= 1u;
+      } else if (issuer) {
         constexpr uint32_t idesc = ptx::idesc_bf16(kBM, BN, 0);
 #pragma unroll
         for (int kk = 0; kk < kRankBK / 16; ++kk)
-          ptx::umma_bf16(tmem + BN, ptx::sdesc_sw128(a + kk * 32, 16, 1024), ptx::sdesc_sw128(b + kk * 32, 16, 1024),
-                         idesc, (i > n1 || kk > 0) ? 1u : 0u);
+          ptx::umma_bf16(tmem + BN, ad + 2 * kk, bd + 2 * kk, idesc, (i > n1 || kk > 0) ? 1u : 0u);
+        ptx::umma_commit(&empty[st]);
       }
-      ptx::umma_commit(&empty[st]);
+      __syncwarp();
+      if (++st == S) st = 0, ph ^= 1u;
       ++done;
     }
     if (done == total) {
-      ptx::umma_commit(accum);
+      if (issuer) ptx::umma_commit(accum);
     } else if (done > 0) {
       // aborted: the issued MMAs finish before tensor memory is freed
-      ptx::umma_commit(drain);
+      if (issuer) ptx::umma_commit(drain);
+      __syncwarp();
       int never = 0;
       ptx::mbar_wait(drain, 0, &never);
     }
@@ -230,19 +248,15 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     const int groups = (n1 + kGroup - 1) / kGroup;
     for (int g = 0; g < groups; ++g) {
       const int ring = g % C::kRing, kb = kb_begin + g * kGroup;
-      const uint32_t wa = scale_word(wsp, 1, kb, kb_end);
-      uint32_t wb[C::kSfbCols];
-#pragma unroll
-      for (int c = 0; c < C::kSfbCols; ++c) {
-        const int m = n_tile * BN + 32 * c + lane;
-        wb[c] = m < args.cols && 32 * c + lane < BN ? scale_word(args.xs + m, args.cols, kb, kb_end) : kOne;
-      }
+      uint32_t wa[1], wb[C::kSfbCols];
+      scale_words(wsp, 1, 0, 0, kb, kb_end - 1, wa);
+      scale_words(args.xs, args.cols, n_tile * BN + lane, args.cols - 1, kb, kb_end - 1, wb);
       bool ok = g < C::kRing || ptx::mbar_wait(&sf_empty[ring], (uint32_t)(g / C::kRing - 1) & 1u, abort_flag);
       if (!ok) give_up();
       if (!__all_sync(0xffffffffu, ok)) break;
       ptx::tc_fence_after();
       const uint32_t sf = tmem + lanes + (uint32_t)(C::kSf + 8 * ring);
-      ptx::tmem_st4(sf, wa, wa, wa, wa);
+      ptx::tmem_st4(sf, wa[0], wa[0], wa[0], wa[0]);
       if constexpr (C::kSfbCols == 4) {
         ptx::tmem_st4(sf + 4, wb[0], wb[1], wb[2], wb[3]);
       } else {
@@ -354,7 +368,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t cta = ptx::cluster_ctarank();  // 0 issues the MMAs
   const int cluster = blockIdx.x / 2, n_clusters = gridDim.x / 2;
   const int n_tiles = (args.cols + kPairN - 1) / kPairN;
@@ -388,7 +402,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
   ptx::tc_fence_before();
   ptx::cluster_sync();  // both CTAs' barriers exist before either signals the other's
   ptx::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const bool early = args.early_start;
   if (!early) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -444,59 +458,64 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         ptx::mbar_wait(&empty[st], (uint32_t)(last / S) & 1u, &never, 100000000ull);
       }
     }
-  } else if (warp == 1 && lane == 0 && cta == 0) {
+  } else if (warp == 1 && cta == 0) {
     // ---------------------------------------------------------- MMA issuer (even CTA)
-    bool stop = false;
-    int g = 0, j = 0, sg = 0, issued = 0;  // stage items, tiles, scale groups
-    for (int tile = cluster; tile < tiles; tile += n_clusters, ++j) {
+    // The whole warp walks the loop, so that addresses and descriptors stay in
+    // uniform registers, and one lane issues (one lane walking it alone spent
+    // 830 cycles a K block on the four MMAs' operands, their time being 480).
+    const bool issuer = ptx::elect_one();
+    const uint64_t desc0 = ptx::sdesc_sw128(ptx::smem_u32(smem), 16, 1024);
+    bool stop = false, any = false;
+    int st = 0, ring = 0;
+    uint32_t ph = 0, ring_ph = 0, free_ph = 1;
+    for (int tile = cluster; tile < tiles && !stop; tile += n_clusters) {
       // the epilogues of both CTAs have read the previous tile's accumulators
-      if (j > 0 && !ptx::mbar_wait(tmem_free, (uint32_t)(j - 1) & 1u, abort_flag)) {
-        give_up();
-        stop = true;
-        break;
-      }
-      ptx::tc_fence_after();
+      bool ok = !any || ptx::mbar_wait(tmem_free, free_ph, abort_flag);
+      free_ph ^= 1u;
       const int N = tile_n(tile);
-      for (int i = 0; i < per_tile; ++i, ++g) {
-        const int st = g % S, ring = sg % kPairRing;
-        bool ok = ptx::mbar_wait(&full[st], (uint32_t)(g / S) & 1u, abort_flag);
-        if (ok && i < n1 && i % kGroup == 0)
-          ok = ptx::mbar_wait(&sf_full[ring], (uint32_t)(sg / kPairRing) & 1u, abort_flag);
-        if (!ok) {
+      const uint32_t idesc1 = ptx::idesc_mxf8(2 * kBM, N, 0), idesc2 = ptx::idesc_bf16(2 * kBM, N, 0);
+      for (int i = 0; i < per_tile; ++i) {
+        const int byte = i % kGroup;
+        ok = ok && ptx::mbar_wait(&full[st], ph, abort_flag);
+        if (ok && i < n1 && byte == 0) ok = ptx::mbar_wait(&sf_full[ring], ring_ph, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) {
           give_up();
           stop = true;
           break;
         }
         ptx::tc_fence_after();
-        const uint32_t a = ptx::smem_u32(smem + st * kPairStageBytes);
-        const uint32_t b = a + kABytes;
+        const uint64_t ad = desc0 + (uint64_t)(st * (kPairStageBytes / 16));
+        const uint64_t bd = ad + kABytes / 16;
         if (i < n1) {
+          const bool last = byte == kGroup - 1 || i == n1 - 1;  // of its scale group
           const uint32_t sf = tmem + (uint32_t)(kPairSf + 16 * ring);
-          const uint32_t idesc = ptx::idesc_mxf8(2 * kBM, N, i % kGroup);
+          const uint32_t idesc = idesc1 | ((uint32_t)byte << 4) | ((uint32_t)byte << 29);
+          if (issuer) {
 #pragma unroll
-          for (int kk = 0; kk < kBK / 32; ++kk)
-            ptx::umma_mxf8<true>(tmem, ptx::sdesc_sw128(a + kk * 32, 16, 1024), ptx::sdesc_sw128(b + kk * 32, 16, 1024),
-                                 idesc, sf, sf + 4, (i > 0 || kk > 0) ? 1u : 0u);
-          if (i % kGroup == kGroup - 1 || i == n1 - 1) {
-            ptx::umma_commit_pair(&sf_empty[ring], kPairMask);
-            ++sg;
+            for (int kk = 0; kk < kBK / 32; ++kk)
+              ptx::umma_mxf8<true>(tmem, ad + 2 * kk, bd + 2 * kk, idesc, sf, sf + 4, (i > 0 || kk > 0) ? 1u : 0u);
+            if (last) ptx::umma_commit_pair(&sf_empty[ring], kPairMask);
+            ptx::umma_commit_pair(&empty[st], kPairMask);
           }
-        } else {
-          const uint32_t idesc = ptx::idesc_bf16(2 * kBM, N, 0);
+          if (last && ++ring == kPairRing) ring = 0, ring_ph ^= 1u;
+        } else if (issuer) {
 #pragma unroll
           for (int kk = 0; kk < kRankBK / 16; ++kk)
-            ptx::umma_bf16_pair(tmem + (uint32_t)kPairN, ptx::sdesc_sw128(a + kk * 32, 16, 1024),
-                                ptx::sdesc_sw128(b + kk * 32, 16, 1024), idesc, (i > n1 || kk > 0) ? 1u : 0u);
+            ptx::umma_bf16_pair(tmem + (uint32_t)kPairN, ad + 2 * kk, bd + 2 * kk, idesc2,
+                                (i > n1 || kk > 0) ? 1u : 0u);
+          ptx::umma_commit_pair(&empty[st], kPairMask);
         }
-        ptx::umma_commit_pair(&empty[st], kPairMask);
-        ++issued;
+        __syncwarp();
+        any = true;
+        if (++st == S) st = 0, ph ^= 1u;
       }
-      if (stop) break;
-      ptx::umma_commit_pair(accum, kPairMask);
+      if (!stop && issuer) ptx::umma_commit_pair(accum, kPairMask);
+      __syncwarp();
     }
-    if (stop && issued > 0) {
+    if (stop && any) {
       // aborted: the issued MMAs finish before tensor memory is released
-      ptx::umma_commit_pair(drain, 0x1);
+      if (issuer) ptx::umma_commit_pair(drain, 0x1);
+      __syncwarp();
       int never = 0;
       ptx::mbar_wait(drain, 0, &never);
     }
@@ -514,20 +533,16 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
       const int tok = (tile % n_tiles) * kPairN + lane;
       for (int q = 0; q < groups; ++q, ++sg) {
         const int ring = sg % kPairRing, kb = q * kGroup;
-        const uint32_t wa = scale_word(wsp, 1, kb, n1);
-        uint32_t wb[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const int m = tok + 32 * c;
-          wb[c] = m < args.cols ? scale_word(args.xs + m, args.cols, kb, n1) : kOne;
-        }
+        uint32_t wa[1], wb[8];
+        scale_words(wsp, 1, 0, 0, kb, n1 - 1, wa);
+        scale_words(args.xs, args.cols, tok, args.cols - 1, kb, n1 - 1, wb);
         ok = sg < kPairRing || ptx::mbar_wait(&sf_empty[ring], (uint32_t)(sg / kPairRing - 1) & 1u, abort_flag);
         if (!ok) give_up();
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ptx::tc_fence_after();
         const uint32_t sf = tmem + lanes + (uint32_t)(kPairSf + 16 * ring);
-        ptx::tmem_st4(sf, wa, wa, wa, wa);
+        ptx::tmem_st4(sf, wa[0], wa[0], wa[0], wa[0]);
         ptx::tmem_st4(sf + 4, wb[0], wb[1], wb[2], wb[3]);
         ptx::tmem_st4(sf + 8, wb[4], wb[5], wb[6], wb[7]);
         ptx::tmem_wait_st();
