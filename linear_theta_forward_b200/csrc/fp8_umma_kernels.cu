@@ -17,11 +17,13 @@
 //   warp 0       TMA producer (one lane): 128 x 128 bytes of W0 codes and the
 //                tile's token codes per stage, 128-byte swizzle
 //   warp 1       tensor-memory allocation; MMA issuer (one lane)
-//   warps 2-5    the scales: bytes from global memory, packed in registers and
-//                written to tensor memory (tcgen05.st), each warp its 32-lane
-//                quarter, a ring of groups ahead of the MMAs
+//   scales       bytes from global memory packed into words. One-SM tiles: warps
+//                2-5 write them to tensor memory (tcgen05.st), each its 32-lane
+//                quarter, a ring of groups ahead of the MMAs. CTA pairs: warps 2
+//                and 3 write them to shared memory, and the MMA issuer copies a
+//                group to tensor memory (tcgen05.cp) in order with its MMAs
 //   epilogue     the same warps 2-5 after the last group (one-SM tiles); warps
-//                6-13 of their own in the persistent CTA-pair kernel
+//                4-11 of their own in the persistent CTA-pair kernel
 // Waits are bounded as everywhere in the library.
 #include <cuda.h>
 
@@ -339,14 +341,20 @@ constexpr int kPairStages = 5;
 constexpr int kPairBBytes = kPairHalf * 128;
 constexpr int kPairStageBytes = kABytes + kPairBBytes;
 constexpr int kPairOutBytes = kBM * kPairN * 2;
-constexpr int kPairSmemBytes = kPairStages * kPairStageBytes + kPairOutBytes + 1024 /*align*/ + 256 /*barriers*/;
 constexpr int kPairSf = 2 * kPairN;  // scale columns: 16 per group, two groups
-constexpr int kPairRing = 2;
+constexpr int kPairRing = 4;         // scale groups in shared memory
+constexpr int kPairSfBytes = 3 * 512;  // of a group: the CTA's 128 rows, then 256 tokens
+constexpr int kPairSmemBytes =
+    kPairStages * kPairStageBytes + kPairOutBytes + kPairRing * kPairSfBytes + 1024 /*align*/ + 256 /*barriers*/;
 constexpr int kPairEpiWarps = 8;
 constexpr int kPairEpi = 32 * kPairEpiWarps;
-constexpr int kPairThreads = 64 + 128 + kPairEpi;
+constexpr int kPairThreads = 128 + kPairEpi;
 constexpr uint16_t kPairMask = 0x3;
-static_assert(kPairSf + 16 * kPairRing <= 512, "accumulators and scales must fit in tensor memory");
+static_assert(kPairSf + 2 * 16 <= 512, "accumulators and scales must fit in tensor memory");
+// The copy of group g + 2 to tensor memory overwrites group g's scales: its
+// first stage's load waited for the MMAs kPairStages items back, and group g + 1
+// has at most kGroup items, so group g's MMAs are done.
+static_assert(kPairStages <= kGroup + 1, "a scale group's columns must be free when they are written again");
 static_assert(kPairBBytes % 1024 == 0, "swizzled tiles start on 1024-byte boundaries");
 
 __global__ void __launch_bounds__(kPairThreads, 1)
@@ -358,7 +366,8 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   bf16* sOut = reinterpret_cast<bf16*>(smem + S * kPairStageBytes);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * kPairStageBytes + kPairOutBytes);
+  uint8_t* sScale = smem + S * kPairStageBytes + kPairOutBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sScale + kPairRing * kPairSfBytes);
   uint64_t* empty = full + S;
   uint64_t* sf_full = empty + S;
   uint64_t* sf_empty = sf_full + kPairRing;
@@ -386,7 +395,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
       ptx::mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < kPairRing; ++i) {
-      ptx::mbar_init(&sf_full[i], 8);  // one arrival per scale warp of both CTAs
+      ptx::mbar_init(&sf_full[i], 2);  // one arrival per CTA
       ptx::mbar_init(&sf_empty[i], 1);
     }
     ptx::mbar_init(accum, 1);
@@ -466,6 +475,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     const bool issuer = ptx::elect_one();
     const uint64_t desc0 = ptx::sdesc_sw128(ptx::smem_u32(smem), 16, 1024);
     bool stop = false, any = false;
+    const uint64_t sf_desc0 = ptx::sdesc_rows16(ptx::smem_u32(sScale));
     int st = 0, ring = 0;
     uint32_t ph = 0, ring_ph = 0, free_ph = 1;
     for (int tile = cluster; tile < tiles && !stop; tile += n_clusters) {
@@ -488,9 +498,14 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         const uint64_t bd = ad + kABytes / 16;
         if (i < n1) {
           const bool last = byte == kGroup - 1 || i == n1 - 1;  // of its scale group
-          const uint32_t sf = tmem + (uint32_t)(kPairSf + 16 * ring);
+          const uint32_t sf = tmem + (uint32_t)(kPairSf + 16 * (ring & 1));
           const uint32_t idesc = idesc1 | ((uint32_t)byte << 4) | ((uint32_t)byte << 29);
           if (issuer) {
+            if (byte == 0) {
+              const uint64_t sd = sf_desc0 + (uint64_t)(ring * (kPairSfBytes / 16));
+#pragma unroll
+              for (int q = 0; q < 3; ++q) ptx::tmem_cp_scales_pair(sf + 4 * q, sd + 32 * q);
+            }
 #pragma unroll
             for (int kk = 0; kk < kBK / 32; ++kk)
               ptx::umma_mxf8<true>(tmem, ad + 2 * kk, bd + 2 * kk, idesc, sf, sf + 4, (i > 0 || kk > 0) ? 1u : 0u);
@@ -519,9 +534,11 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
       int never = 0;
       ptx::mbar_wait(drain, 0, &never);
     }
-  } else if (warp >= 2 && warp < 6) {
+  } else if (warp == 2 || warp == 3) {
     // ---------------------------------------------------------- scales (both CTAs)
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    // Groups in turn between the two warps: lane l writes the words of rows l,
+    // 32 + l, 64 + l and 96 + l, 16 bytes for the W0 rows (all alike) and twice
+    // 16 for the tokens.
     const uint32_t full_bar = ptx::mapa(ptx::smem_u32(sf_full), 0);
     const int row_blocks = (args.rows + kBM - 1) / kBM;
     bool ok = true;
@@ -532,6 +549,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
       const uint8_t* wsp = args.ws + (int64_t)rb * args.kb1;
       const int tok = (tile % n_tiles) * kPairN + lane;
       for (int q = 0; q < groups; ++q, ++sg) {
+        if ((sg & 1) != (warp & 1)) continue;
         const int ring = sg % kPairRing, kb = q * kGroup;
         uint32_t wa[1], wb[8];
         scale_words(wsp, 1, 0, 0, kb, n1 - 1, wa);
@@ -540,24 +558,25 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         if (!ok) give_up();
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        ptx::tc_fence_after();
-        const uint32_t sf = tmem + lanes + (uint32_t)(kPairSf + 16 * ring);
-        ptx::tmem_st4(sf, wa[0], wa[0], wa[0], wa[0]);
-        ptx::tmem_st4(sf + 4, wb[0], wb[1], wb[2], wb[3]);
-        ptx::tmem_st4(sf + 8, wb[4], wb[5], wb[6], wb[7]);
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
+        uint4* dst = reinterpret_cast<uint4*>(sScale + ring * kPairSfBytes) + lane;
+        dst[0] = make_uint4(wa[0], wa[0], wa[0], wa[0]);
+        dst[32] = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+        dst[64] = make_uint4(wb[4], wb[5], wb[6], wb[7]);
+        ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive_cluster(full_bar + (uint32_t)(ring * 8));
       }
     }
-  } else if (warp >= 6) {
+  } else if (warp >= 4) {
     // ---------------------------------------------------------- epilogue (both CTAs)
+    // The tile is rounded to bf16 in registers and tensor memory handed back
+    // before anything is written to shared memory: the MMAs wait for the
+    // tensor-memory reads alone.
     const int quarter = warp & 3;         // a warp reads lanes 32 * (warp % 4) ...
-    const int part = (warp - 6) / 4;      // ... and columns [128 * part, ...)
+    const int part = (warp - 4) / 4;      // ... and columns 128 * part ...
     const int row = quarter * 32 + lane;  // accumulator row = tensor-memory lane
-    const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16);
-    const bool storer = threadIdx.x == 192;  // issues the TMA stores of the tile
+    const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(part * 128);
+    const bool storer = threadIdx.x == 128;  // issues the TMA stores of the tile
     const uint32_t free_bar = ptx::mapa(ptx::smem_u32(tmem_free), 0);
     if (early) asm volatile("griddepcontrol.wait;" ::: "memory");
     bool ok = true;
@@ -565,29 +584,47 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     for (int tile = cluster; tile < tiles; tile += n_clusters, ++j) {
       const int row0 = (tile / n_tiles) * (2 * kBM) + (int)cta * kBM;
       const int col0 = (tile % n_tiles) * kPairN;
-      const int ncols = min(kPairN, args.cols - col0);
+      const int ncols = min(kPairN, args.cols - col0) - part * 128;  // of this warp's columns
+      const int grow = row0 + row;
+      const float so = grow < args.rows ? args.s[grow] : 0.f;
+      const bool got = __all_sync(0xffffffffu, ptx::mbar_wait(accum, (uint32_t)j & 1u, abort_flag));
+      uint32_t y[64];
+      if (got) {
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float d1[32], d2[32];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // columns past the tile's tokens are not read
+            if (32 * q + 16 * h < ncols) {
+              ptx::tmem_ld16(taddr + 32 * q + 16 * h, *reinterpret_cast<float(*)[16]>(d1 + 16 * h));
+              if (has_d2)
+                ptx::tmem_ld16(taddr + kPairN + 32 * q + 16 * h, *reinterpret_cast<float(*)[16]>(d2 + 16 * h));
+            }
+          }
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            y[16 * q + e] = has_d2 ? pack_bf16x2(fmaf(so, d1[2 * e], d2[2 * e]), fmaf(so, d1[2 * e + 1], d2[2 * e + 1]))
+                                   : pack_bf16x2(so * d1[2 * e], so * d1[2 * e + 1]);
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(free_bar);
+      }
       if (storer) ptx::bulk_wait_read();  // the previous tile's store has read sOut
-      const bool got = ptx::mbar_wait(accum, (uint32_t)j & 1u, abort_flag);
-      // one decision for all epilogue warps: the barriers below need every one of them
+      // one decision for all epilogue warps: the barriers need every one of them
       ok = ptx::bar_red_and(1, kPairEpi, got);
       if (!ok) break;
-      ptx::tc_fence_after();
-      const int grow = row0 + row;
-      const float so = grow < args.rows ? __ldg(args.s + grow) : 0.f;
-      const int c_end = min(ncols, part * 128 + 128);
-      for (int c0 = part * 128; c0 < c_end; c0 += 16) {
-        float d1[16], d2[16];
-        ptx::tmem_ld16(taddr + c0, d1);
-        if (has_d2) ptx::tmem_ld16(taddr + kPairN + c0, d2);
-        ptx::tmem_wait_ld();
+      uint16_t* dst = reinterpret_cast<uint16_t*>(sOut) + part * 128 * kBM + row;
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          sOut[(c0 + e) * kBM + row] = __float2bfloat16_rn(has_d2 ? fmaf(so, d1[e], d2[e]) : so * d1[e]);
+      for (int e = 0; e < 64; ++e) {
+        if (2 * e < ncols) {
+          dst[2 * e * kBM] = (uint16_t)y[e];
+          dst[(2 * e + 1) * kBM] = (uint16_t)(y[e] >> 16);
+        }
       }
-      // tensor memory read: the next tile's MMAs may start
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster(free_bar);
       ptx::fence_proxy_async_smem();
       asm volatile("bar.sync 1, %0;" ::"n"(kPairEpi) : "memory");
       if (storer && row0 < args.rows) {

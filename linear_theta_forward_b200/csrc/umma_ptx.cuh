@@ -318,6 +318,19 @@ __host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N, int byte) {
          ((uint32_t)byte << 29);
 }
 
+// Copies 512 bytes of shared memory -- 32 rows of 16 bytes, no swizzle -- to
+// four columns of tensor memory: row l to lane l of every 32-lane quarter, in
+// both CTAs of the pair from each one's own shared memory at this offset.
+// Runs in order with the MMAs that the same thread issues after it.
+__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+// Its source descriptor: groups of 8 rows (128 bytes) one after another.
+__device__ __forceinline__ uint64_t sdesc_rows16(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 16) | ((uint64_t)(128 >> 4) << 32) |
+         (1ull << 46);
+}
+
 // Stores of 32 lanes x 32 bits, consecutive columns per thread.
 __device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v) : "memory");
