@@ -18,6 +18,7 @@
 // their full precision; the block computes one sine and cosine per pair and
 // token, shared by its heads.
 #include <algorithm>
+#include <mutex>
 
 #include "common.cuh"
 #include "internal.h"
@@ -30,25 +31,47 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxDim = 1024;
 
+// How a value finds its pair's other value: halves of whole 8-value vectors,
+// neighbours, or halves that cut a vector.
+enum Pairing { HALVES = 0, NEIGHBOURS = 1, ODD_HALVES = 2 };
+
 struct HeadArgs {
   HeadSide side[2];  // queries, keys
   const int64_t* pos;
   const float* inv_freq;
+  int64_t M;
   int D, rotary;
-  int aligned;  // half-split pairs whose halves are whole 8-value vectors
   float offset, eps;
-  int per_block;  // heads (queries then keys) of one block
+  int warps;      // warps per token: a block works on kWarps / warps tokens at a time
+  int per_block;  // heads (queries then keys) of a token that one block takes
 };
 
+// 8 values as loaded: 16 bytes of bf16, 32 of fp32.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&f)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    unpack(*reinterpret_cast<const uint4*>(p), f);
-  } else {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+struct Raw8 {
+  static constexpr int kWords = 2 * sizeof(T);
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+    const uint4 a = reinterpret_cast<const uint4*>(p)[0];
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+    if constexpr (sizeof(T) == 4) {
+      const uint4 b = reinterpret_cast<const uint4*>(p)[1];
+      w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    }
   }
-}
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    if constexpr (sizeof(T) == 2) {
+      unpack(make_uint4(w[0], w[1], w[2], w[3]), f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+    }
+  }
+};
 
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
@@ -60,135 +83,227 @@ __device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
   }
 }
 
+template <typename T>
+__device__ __forceinline__ void weights8(const T* w, int i, float offset, float (&f)[8]) {
+  if (!w) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = 1.f;
+    return;
+  }
+  Raw8<T> r;
+  r.load(w + i);
+  r.get(f);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] += offset;
+}
+
+// Sine and cosine of the token's angle of pair i. The angle in turns, whole
+// and quarter turns taken off exactly in fp64; what is left is at most an
+// eighth of a turn, so its fp32 rounding is below 2^-25 of a radian.
+__device__ __forceinline__ void angle(double turns, float freq, float* c, float* s) {
+  const double t4 = 4.0 * (turns * (double)freq);
+  const double k = rint(t4);
+  float s0, c0;
+  sincospif(0.5f * (float)(t4 - k), &s0, &c0);
+  const int quarter = (int)((long long)k & 3);
+  const float c1 = quarter & 1 ? -s0 : c0, s1 = quarter & 1 ? c0 : s0;
+  *c = quarter & 2 ? -c1 : c1;
+  *s = quarter & 2 ? -s1 : s1;
+}
+
 // G lanes a head, VPL vectors of 8 values a lane.
-template <typename T, int G, int VPL, bool INTERLEAVED>
+template <typename T, int G, int VPL, int PAIRING>
 __global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__ HeadArgs a) {
-  __shared__ float cs[kMaxDim / 2], sn[kMaxDim / 2];
+  extern __shared__ float table[];  // two buffers of [tokens][cos, sin][rotary / 2]
+  constexpr int kAhead = VPL == 1 ? 4 : VPL == 2 ? 2 : 1;  // heads a lane loads at once
   const int64_t* pos = a.pos;
   const float* freq = a.inv_freq;
   pdl_enter(pos, freq);
-  const int64_t m = blockIdx.x;
-  const int half = a.rotary / 2;
-  if (half > 0) {
-    const double turns0 = (double)pos[m] * 0.15915494309189535;  // position / 2 pi
-    for (int i = threadIdx.x; i < half; i += kThreads) {
-      // the nearest quarter turn k and what is left of it, exact in fp64; the
-      // remainder is at most an eighth of a turn, so its fp32 rounding is
-      // below 2^-25 of a radian
-      const double t4 = 4.0 * (turns0 * (double)freq[i]);
-      const double k = rint(t4);
-      float s, co;
-      sincospif(0.5f * (float)(t4 - k), &s, &co);
-      const int quarter = (int)((long long)k & 3);
-      const float c1 = quarter & 1 ? -s : co, s1 = quarter & 1 ? co : s;
-      cs[i] = quarter & 2 ? -c1 : c1;
-      sn[i] = quarter & 2 ? -s1 : s1;
-    }
-    __syncthreads();
-  }
-  constexpr int kGroups = kThreads / G;  // heads a block works on at once
-  const int grp = threadIdx.x / G, lane = threadIdx.x % G;
+  const int D = a.D, rotary = a.rotary, half = rotary / 2;
+  const int tokens = kWarps / a.warps;                     // of a block at a time
+  const int mine = threadIdx.x / 32 / a.warps;             // this warp's among them
+  const int groups = a.warps * (32 / G);                   // heads of a token worked on at once
+  const int grp = threadIdx.x % (32 * a.warps) / G, lane = threadIdx.x % G;
   const unsigned mask = G == 32 ? 0xffffffffu : ((1u << G) - 1u) << (threadIdx.x % 32 / G * G);
-  const int D = a.D;
-  int h = (int)blockIdx.y * a.per_block;
-  const int h_end = min(h + a.per_block, a.side[0].heads + a.side[1].heads);
-  for (int w = 0; w < 2; ++w) {
-    // this block's heads of this side
-    const int base = w == 0 ? 0 : a.side[0].heads;
-    const int lo = max(h, base), hi = min(h_end, base + a.side[w].heads);
-    if (lo >= hi) continue;
-    const T* x0 = static_cast<const T*>(a.side[w].x) + m * a.side[w].ld;
-    T* y0 = static_cast<T*>(a.side[w].y) + m * a.side[w].ld_out;
-    const T* wt = static_cast<const T*>(a.side[w].weight);
-    after_wait(x0), after_wait(wt);
-    float A[VPL][8], B[VPL][8];
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-      const int i0 = (lane + v * G) * 8;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int i = i0 + e;
-        A[v][e] = B[v][e] = 0.f;
-        if (i >= D) continue;
-        const float wi = wt ? to_f32(wt[i]) + a.offset : 1.f;
-        if (i < a.rotary) {
-          const bool second = INTERLEAVED ? (i & 1) : i >= half;
-          const int pair = INTERLEAVED ? i / 2 : second ? i - half : i;
-          const int j = INTERLEAVED ? i ^ 1 : second ? i - half : i + half;
-          const float wj = wt ? to_f32(wt[j]) + a.offset : 1.f;
-          A[v][e] = wi * cs[pair];
-          B[v][e] = second ? wj * sn[pair] : -wj * sn[pair];
-        } else {
-          A[v][e] = wi;
-        }
+  const int h_lo = (int)blockIdx.y * a.per_block, h_hi = min(h_lo + a.per_block, a.side[0].heads + a.side[1].heads);
+  int buf = 0;
+  for (int64_t m0 = (int64_t)blockIdx.x * tokens; m0 < a.M; m0 += (int64_t)gridDim.x * tokens, buf ^= 1) {
+    float* tab = table + buf * tokens * rotary;
+    if (half > 0) {
+      for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
+        const int t = i / half, p = i - t * half;
+        const int64_t m = min(m0 + t, a.M - 1);
+        angle((double)pos[m] * 0.15915494309189535, freq[p], &tab[t * rotary + p], &tab[t * rotary + half + p]);
       }
+      // one barrier a round: the buffer written next round was last read the
+      // round before this barrier
+      __syncthreads();
     }
-    for (int hh = lo + grp; hh < hi; hh += kGroups) {
-      const T* x = x0 + (int64_t)(hh - base) * D;
-      float f[VPL][8], p[VPL][8];
-      float ss = 0.f;
+    const int64_t m = m0 + mine;
+    if (m >= a.M) continue;
+    const float* cs = tab + mine * rotary;
+    const float* sn = cs + half;
+    for (int w = 0; w < 2; ++w) {
+      // this block's heads of this side
+      const int base = w == 0 ? 0 : a.side[0].heads;
+      const int lo = max(h_lo, base), hi = min(h_hi, base + a.side[w].heads);
+      if (lo >= hi) continue;
+      const T* x0 = static_cast<const T*>(a.side[w].x) + m * a.side[w].ld;
+      T* y0 = static_cast<T*>(a.side[w].y) + m * a.side[w].ld_out;
+      const T* wt = static_cast<const T*>(a.side[w].weight);
+      after_wait(x0), after_wait(wt);
+      float A[VPL][8], B[VPL][8];
 #pragma unroll
       for (int v = 0; v < VPL; ++v) {
         const int i0 = (lane + v * G) * 8;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[v][e] = p[v][e] = 0.f;
-        if (i0 < D) {
-          load8(x + i0, f[v]);
-          if constexpr (INTERLEAVED) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (i0 + e < a.rotary) p[v][e] = f[v][e ^ 1];
-          } else if (a.aligned) {
-            if (i0 < a.rotary) load8(x + (i0 < half ? i0 + half : i0 - half), p[v]);
-          } else {
+        for (int e = 0; e < 8; ++e) A[v][e] = B[v][e] = 0.f;
+        if (i0 >= D) continue;
+        weights8(wt, i0, a.offset, A[v]);
+        if constexpr (PAIRING == HALVES) {
+          if (i0 < rotary) {
+            const bool second = i0 >= half;
+            const int p0 = second ? i0 - half : i0;
+            weights8(wt, second ? p0 : i0 + half, a.offset, B[v]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const int i = i0 + e;
-              if (i < a.rotary) p[v][e] = to_f32(x[i < half ? i + half : i - half]);
+              A[v][e] *= cs[p0 + e];
+              B[v][e] *= second ? sn[p0 + e] : -sn[p0 + e];
+            }
+          }
+        } else if constexpr (PAIRING == NEIGHBOURS) {
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            if (i0 + e < rotary) {
+              const float c = cs[i0 / 2 + e / 2], s = sn[i0 / 2 + e / 2], w0 = A[v][e], w1 = A[v][e + 1];
+              A[v][e] = w0 * c, B[v][e] = -w1 * s;
+              A[v][e + 1] = w1 * c, B[v][e + 1] = w0 * s;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int i = i0 + e;
+            if (i < rotary) {
+              const bool second = i >= half;
+              const int p = second ? i - half : i, j = second ? p : i + half;
+              const float wj = wt ? to_f32(wt[j]) + a.offset : 1.f;
+              A[v][e] *= cs[p];
+              B[v][e] = second ? wj * sn[p] : -wj * sn[p];
+            }
+          }
+        }
+      }
+      for (int h0 = lo + grp; h0 < hi; h0 += kAhead * groups) {
+        Raw8<T> raw[kAhead][VPL], other[PAIRING == HALVES && VPL > 1 ? kAhead : 1][VPL];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const T* x = x0 + (int64_t)(h0 + u * groups - base) * D;
+#pragma unroll
+          for (int v = 0; v < VPL; ++v) {
+            const int i0 = (lane + v * G) * 8;
+            raw[u][v].zero();
+            if (i0 < D && h0 + u * groups < hi) raw[u][v].load(x + i0);
+            if constexpr (PAIRING == HALVES && VPL > 1) {
+              other[u][v].zero();
+              if (i0 < rotary && h0 + u * groups < hi) other[u][v].load(x + (i0 < half ? i0 + half : i0 - half));
             }
           }
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(f[v][e], f[v][e], ss);
-      }
-      // every lane of the group has read the head before any lane writes it
-      // (the outputs may be the inputs): the shuffles order them
+        for (int u = 0; u < kAhead; ++u) {
+          if (h0 + u * groups >= hi) break;
+          const int64_t at = (int64_t)(h0 + u * groups - base) * D;
+          float f[VPL][8], p[VPL][8];
+          float ss = 0.f;
 #pragma unroll
-      for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-      __syncwarp(mask);
-      const float r = rsqrtf(ss / (float)D + a.eps);
+          for (int v = 0; v < VPL; ++v) {
+            const int i0 = (lane + v * G) * 8;
+            raw[u][v].get(f[v]);
+            if constexpr (PAIRING == HALVES && VPL == 1) {
+              // the other half's vector is another lane's
+              const int from = i0 >= rotary ? lane : i0 < half ? lane + half / 8 : lane - half / 8;
+              Raw8<T> o;
 #pragma unroll
-      for (int v = 0; v < VPL; ++v) {
-        const int i0 = (lane + v * G) * 8;
-        if (i0 >= D) continue;
-        float y[8];
+              for (int q = 0; q < Raw8<T>::kWords; ++q) o.w[q] = __shfl_sync(mask, raw[u][v].w[q], from, G);
+              if (i0 >= rotary) o.zero();
+              o.get(p[v]);
+            } else if constexpr (PAIRING == HALVES) {
+              other[u][v].get(p[v]);
+            } else if constexpr (PAIRING == NEIGHBOURS) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = r * fmaf(f[v][e], A[v][e], p[v][e] * B[v][e]);
-        store8(y0 + (int64_t)(hh - base) * D + i0, y);
+              for (int e = 0; e < 8; ++e) p[v][e] = i0 + e < rotary ? f[v][e ^ 1] : 0.f;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int i = i0 + e;
+                p[v][e] = i < rotary ? to_f32(x0[at + (i < half ? i + half : i - half)]) : 0.f;
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(f[v][e], f[v][e], ss);
+          }
+#pragma unroll
+          for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
+          // every lane of the group has read the head before any lane writes
+          // it (the outputs may be the inputs)
+          __syncwarp(mask);
+          const float r = rsqrtf(ss / (float)D + a.eps);
+#pragma unroll
+          for (int v = 0; v < VPL; ++v) {
+            const int i0 = (lane + v * G) * 8;
+            if (i0 >= D) continue;
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = r * fmaf(f[v][e], A[v][e], p[v][e] * B[v][e]);
+            store8(y0 + at + i0, y);
+          }
+        }
       }
     }
   }
 }
 
-template <typename T, int G, int VPL>
-cudaError_t launch_heads(const LaunchCtx& c, const HeadArgs& a, int64_t M, bool interleaved) {
+template <typename T, int G, int VPL, int PAIRING>
+cudaError_t launch_heads(const LaunchCtx& c, HeadArgs a) {
+  auto kern = heads_kernel<T, G, VPL, PAIRING>;
+  static int resident[64] = {};
+  int per_sm;
+  {
+    std::lock_guard<std::mutex> lk(setup_mutex());
+    int& slot = resident[c.device];
+    if (!slot && (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&slot, kern, kThreads, 4 * kMaxDim) != cudaSuccess ||
+                  slot < 1))
+      slot = 1;
+    per_sm = slot;
+  }
   const int heads = a.side[0].heads + a.side[1].heads;
-  HeadArgs b = a;
-  // few tokens: one pass of heads a block, so that the heads spread over the GPU
-  b.per_block = M < 2 * (int64_t)c.num_sms ? std::min(heads, kThreads / G) : heads;
-  const dim3 grid((unsigned)M, (unsigned)ceil_div(heads, b.per_block));
-  return interleaved
-             ? launch_pdl(heads_kernel<T, G, VPL, true>, grid, dim3(kThreads), 0, c.stream, 1, b)
-             : launch_pdl(heads_kernel<T, G, VPL, false>, grid, dim3(kThreads), 0, c.stream, 1, b);
+  // Few tokens: a block a token and pass of heads, so that the heads spread
+  // over the GPU. Many: two warps a token, which share its angles and factors
+  // over more heads, in one wave of blocks.
+  const bool few = a.M < 2 * (int64_t)c.num_sms;
+  a.warps = few ? kWarps : 2;
+  a.per_block = few ? std::min(heads, kThreads / G) : heads;
+  const int tokens = kWarps / a.warps;
+  const int64_t blocks = ceil_div(a.M, tokens);
+  const dim3 grid((unsigned)(few ? blocks : std::min<int64_t>(blocks, (int64_t)c.num_sms * per_sm)),
+                  (unsigned)ceil_div(heads, a.per_block));
+  return launch_pdl(kern, grid, dim3(kThreads), (size_t)2 * tokens * a.rotary * sizeof(float), c.stream, 1, a);
+}
+
+template <typename T, int G, int VPL>
+cudaError_t launch_pairing(const LaunchCtx& c, const HeadArgs& a, bool interleaved) {
+  if (interleaved) return launch_heads<T, G, VPL, NEIGHBOURS>(c, a);
+  return a.rotary % 16 == 0 ? launch_heads<T, G, VPL, HALVES>(c, a) : launch_heads<T, G, VPL, ODD_HALVES>(c, a);
 }
 
 template <typename T>
-cudaError_t launch_dim(const LaunchCtx& c, const HeadArgs& a, int64_t M, bool interleaved) {
-  if (a.D <= 64) return launch_heads<T, 8, 1>(c, a, M, interleaved);
-  if (a.D <= 128) return launch_heads<T, 16, 1>(c, a, M, interleaved);
-  if (a.D <= 256) return launch_heads<T, 32, 1>(c, a, M, interleaved);
-  if (a.D <= 512) return launch_heads<T, 32, 2>(c, a, M, interleaved);
-  return launch_heads<T, 32, 4>(c, a, M, interleaved);
+cudaError_t launch_dim(const LaunchCtx& c, const HeadArgs& a, bool interleaved) {
+  if (a.D <= 64) return launch_pairing<T, 8, 1>(c, a, interleaved);
+  if (a.D <= 128) return launch_pairing<T, 16, 1>(c, a, interleaved);
+  if (a.D <= 256) return launch_pairing<T, 32, 1>(c, a, interleaved);
+  if (a.D <= 512) return launch_pairing<T, 32, 2>(c, a, interleaved);
+  return launch_pairing<T, 32, 4>(c, a, interleaved);
 }
 
 }  // namespace
@@ -203,12 +318,12 @@ cudaError_t launch_qk_norm_rope(const LaunchCtx& c, theta_dtype dt, const HeadSi
   a.side[1] = k;
   a.pos = positions;
   a.inv_freq = inv_freq;
+  a.M = M;
   a.D = head_dim;
   a.rotary = rotary;
-  a.aligned = rotary % 16 == 0;
   a.offset = offset;
   a.eps = eps;
-  return dt == THETA_BF16 ? launch_dim<bf16>(c, a, M, interleaved) : launch_dim<float>(c, a, M, interleaved);
+  return dt == THETA_BF16 ? launch_dim<bf16>(c, a, interleaved) : launch_dim<float>(c, a, interleaved);
 }
 
 }  // namespace theta
