@@ -37,16 +37,11 @@ __device__ __forceinline__ int scale_byte(float amax) {
 // 2^(127 - byte), the reciprocal of the scale (byte <= 247: always normal).
 __device__ __forceinline__ float inverse_scale(int byte) { return __uint_as_float((uint32_t)(254 - byte) << 23); }
 
-__device__ __forceinline__ float finite_abs_max(float mx, float x) {
-  const float a = fabsf(x);
-  return a <= kMaxFinite ? fmaxf(mx, a) : mx;
-}
-
 __device__ __forceinline__ float scaled(float x, float inv) {
   return fabsf(x) <= kMaxFinite ? x * inv : __uint_as_float(0x7fffffffu);
 }
 
-// E4M3 codes of four values, the first in the low byte.
+// E4M3 codes of four values, the first in the low byte. A NaN gives 0x7f.
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
   uint16_t lo, hi;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
@@ -54,79 +49,155 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-__device__ __forceinline__ uint2 encode8(const float (&f)[8], float inv) {
-  float v[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = scaled(f[e], inv);
-  return make_uint2(encode4(v[0], v[1], v[2], v[3]), encode4(v[4], v[5], v[6], v[7]));
-}
-
 // 8 values as loaded (16 bytes of bf16, 32 of fp32), kept packed so that a
 // thread can hold many of them in flight.
+//   abs_max   the largest magnitude, NaN ignored, infinities not
+//   encode    the codes of x * inv, for values without infinities
+// The encoders are bound by instructions as much as by HBM, so bf16 is worked
+// on in pairs: the maximum, and the product with a power of two, which is
+// exact in bf16 (results below its smallest normal number encode to 0 either
+// way).
 template <typename T>
 struct Raw8;
 template <>
 struct Raw8<bf16> {
-  uint4 v;
-  __device__ __forceinline__ void load(const bf16* p) { v = __ldcs(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void get(float (&f)[8]) const { unpack(v, f); }
+  __nv_bfloat162 v[4];
+  __device__ __forceinline__ void load(const bf16* p) {
+    *reinterpret_cast<uint4*>(v) = __ldcs(reinterpret_cast<const uint4*>(p));
+  }
+  __device__ __forceinline__ void zero() { *reinterpret_cast<uint4*>(v) = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&f)[8]) const { unpack(*reinterpret_cast<const uint4*>(v), f); }
+  static __device__ __forceinline__ __nv_bfloat162 max_init() { return __floats2bfloat162_rn(0.f, 0.f); }
+  __device__ __forceinline__ void abs_max(__nv_bfloat162& m) const {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) m = __hmax2(m, __habs2(v[q]));
+  }
+  static __device__ __forceinline__ float max_value(const __nv_bfloat162& m) {
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+  __device__ __forceinline__ uint2 encode(float inv) const {
+    const __nv_bfloat162 k = __float2bfloat162_rn(inv);
+    float f[8];
+    uint4 s;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&s);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const __nv_bfloat162 y = __hmul2_rn(v[q], k);
+      w[q] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+    unpack(s, f);
+    return make_uint2(encode4(f[0], f[1], f[2], f[3]), encode4(f[4], f[5], f[6], f[7]));
+  }
 };
 template <>
 struct Raw8<float> {
-  float4 a, b;
+  float v[8];
   __device__ __forceinline__ void load(const float* p) {
-    a = __ldcs(reinterpret_cast<const float4*>(p));
-    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+  }
   __device__ __forceinline__ void get(float (&f)[8]) const {
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = v[e];
+  }
+  static __device__ __forceinline__ float max_init() { return 0.f; }
+  __device__ __forceinline__ void abs_max(float& m) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
+  }
+  static __device__ __forceinline__ float max_value(float m) { return m; }
+  __device__ __forceinline__ uint2 encode(float inv) const {
+    return make_uint2(encode4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                      encode4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
   }
 };
+
+// The rare form, for a block that holds an infinity: magnitudes and codes
+// value by value.
+template <typename T>
+__device__ __noinline__ float finite_abs_max(const Raw8<T>& r, float mx) {
+  float f[8];
+  r.get(f);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) mx = fabsf(f[e]) <= kMaxFinite ? fmaxf(mx, fabsf(f[e])) : mx;
+  return mx;
+}
+template <typename T>
+__device__ __noinline__ uint2 encode_checked(const Raw8<T>& r, float inv) {
+  float v[8];
+  r.get(v);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = scaled(v[e], inv);
+  return make_uint2(encode4(v[0], v[1], v[2], v[3]), encode4(v[4], v[5], v[6], v[7]));
+}
 
 // One CTA per 128 x 128 block of W0: a thread holds 8 vectors of 8 values
 // (rows t / 16 + 16 j), so the block is read once, with all its loads in
 // flight, and written from registers.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(const T* __restrict__ W, int64_t O, int64_t I,
-                                                                uint8_t* __restrict__ codes,
-                                                                uint8_t* __restrict__ scales) {
-  __shared__ float red[kThreads / 32];
-  pdl_enter(W);
-  const int64_t nb = ceil_div(I, kBlock);
-  const int64_t bo = blockIdx.x / nb, bi = blockIdx.x % nb;
-  const int64_t r0 = bo * kBlock + threadIdx.x / 16, col = bi * kBlock + (threadIdx.x % 16) * 8;
-  Raw8<T> raw[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (r0 + 16 * j < O && col < I)
-      raw[j].load(W + (r0 + 16 * j) * I + col);
-    else
-      raw[j].zero();
-  }
-  float mx = 0.f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    float f[8];
-    raw[j].get(f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) mx = finite_abs_max(mx, f[e]);
-  }
+// The largest magnitude of the CTA's values: `mx` reduced over its threads.
+__device__ __forceinline__ float cta_max(float mx, float* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = mx;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kThreads / 32; ++i) mx = fmaxf(mx, red[i]);
-  const int byte = scale_byte(mx);
-  const float inv = inverse_scale(byte);
+  return mx;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
+fp8_quantize_kernel(const T* __restrict__ W, int64_t O, int64_t I, uint8_t* __restrict__ codes,
+                    uint8_t* __restrict__ scales) {
+  __shared__ float red[2][kThreads / 32];
+  pdl_enter(W);
+  const int64_t nb = ceil_div(I, kBlock);
+  const int64_t bo = blockIdx.x / nb, bi = blockIdx.x % nb;
+  const int64_t r0 = bo * kBlock + threadIdx.x / 16, col = bi * kBlock + (threadIdx.x % 16) * 8;
+  const int rows = col < I ? (int)max((int64_t)0, min((int64_t)8, ceil_div(O - r0, 16))) : 0;  // of this thread
+  const T* src = W + r0 * I + col;
+  Raw8<T> raw[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    if (r0 + 16 * j >= O || col >= I) continue;
-    float f[8];
-    raw[j].get(f);
-    *reinterpret_cast<uint2*>(codes + (r0 + 16 * j) * I + col) = encode8(f, inv);
+    if (j < rows)
+      raw[j].load(src + j * 16 * I);
+    else
+      raw[j].zero();
+  }
+  auto m = Raw8<T>::max_init();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) raw[j].abs_max(m);
+  float mx = cta_max(Raw8<T>::max_value(m), red[0]);
+  const bool rare = mx > kMaxFinite;
+  if (rare) {
+    mx = 0.f;
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j) {
+      Raw8<T> x;  // read again: indexing raw[] here would put it in local memory
+      x.zero();
+      if (j < rows) x.load(src + j * 16 * I);
+      mx = finite_abs_max(x, mx);
+    }
+    mx = cta_max(mx, red[1]);
+  }
+  const int byte = scale_byte(mx);
+  const float inv = inverse_scale(byte);
+  uint8_t* dst = codes + r0 * I + col;
+  if (!rare) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < rows) *reinterpret_cast<uint2*>(dst + j * 16 * I) = raw[j].encode(inv);
+  } else {
+#pragma unroll 1
+    for (int j = 0; j < rows; ++j) {
+      Raw8<T> x;
+      x.load(src + j * 16 * I);
+      *reinterpret_cast<uint2*>(dst + j * 16 * I) = encode_checked(x, inv);
+    }
   }
   if (threadIdx.x == 0) scales[bo * nb + bi] = (uint8_t)byte;
 }
@@ -139,34 +210,42 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_rows_kernel(const T* __
                                                                      uint8_t* __restrict__ codes,
                                                                      uint8_t* __restrict__ scales) {
   pdl_enter(X);
-  const int64_t nb = ceil_div(I, kBlock), units = ceil_div(nb, kRowBlocks);
-  const int64_t unit = (int64_t)blockIdx.x * (kThreads / 16) + threadIdx.x / 16;
-  const int64_t m = unit / units, b0 = unit % units * kRowBlocks;
-  const bool live = m < M;
+  const uint32_t nb = (uint32_t)ceil_div(I, kBlock), units = (nb + kRowBlocks - 1) / kRowBlocks;
+  const uint32_t unit = blockIdx.x * (kThreads / 16) + threadIdx.x / 16;  // host: fewer than 2^31
+  const uint32_t m = unit / units, b0 = (unit - m * units) * kRowBlocks;
   const int lane = threadIdx.x % 16;
+  const int64_t at = (int64_t)m * I + (int64_t)b0 * kBlock + lane * 8;
+  // this lane's vectors inside the row
+  const int live = m < M ? (int)max((int64_t)0, min((int64_t)kRowBlocks,
+                                                     ceil_div(I - (int64_t)b0 * kBlock - lane * 8, kBlock)))
+                         : 0;
   Raw8<T> raw[kRowBlocks];
 #pragma unroll
   for (int j = 0; j < kRowBlocks; ++j) {
-    const int64_t col = (b0 + j) * kBlock + lane * 8;
-    if (live && col < I)
-      raw[j].load(X + m * I + col);
+    if (j < live)
+      raw[j].load(X + at + j * kBlock);
     else
       raw[j].zero();
   }
 #pragma unroll
   for (int j = 0; j < kRowBlocks; ++j) {
-    const int64_t col = (b0 + j) * kBlock + lane * 8;
-    float f[8];
-    raw[j].get(f);
-    float mx = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) mx = finite_abs_max(mx, f[e]);
+    auto mp = Raw8<T>::max_init();
+    raw[j].abs_max(mp);
+    float mx = Raw8<T>::max_value(mp);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const bool rare = mx > kMaxFinite;  // the same in the block's 16 lanes
+    if (__any_sync(0xffffffffu, rare)) {
+      float fm = finite_abs_max(raw[j], 0.f);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) fm = fmaxf(fm, __shfl_xor_sync(0xffffffffu, fm, o));
+      mx = fm;
+    }
     const int byte = scale_byte(mx);
-    if (live && col < I) {
-      *reinterpret_cast<uint2*>(codes + m * I + col) = encode8(f, inverse_scale(byte));
-      if (lane == 0) scales[(b0 + j) * M + m] = (uint8_t)byte;
+    const float inv = inverse_scale(byte);
+    if (j < live) {
+      *reinterpret_cast<uint2*>(codes + at + j * kBlock) = rare ? encode_checked(raw[j], inv) : raw[j].encode(inv);
+      if (lane == 0) scales[(int64_t)(b0 + j) * M + m] = (uint8_t)byte;
     }
   }
 }

@@ -73,6 +73,26 @@ struct Raw8 {
   }
 };
 
+// Pairs of fp32 in one register pair: two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ void split2(uint64_t p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
   if constexpr (sizeof(T) == 2) {
@@ -120,6 +140,7 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__
   const float* freq = a.inv_freq;
   pdl_enter(pos, freq);
   const int D = a.D, rotary = a.rotary, half = rotary / 2;
+  const float inv_d = 1.f / (float)D;
   const int tokens = kWarps / a.warps;                     // of a block at a time
   const int mine = threadIdx.x / 32 / a.warps;             // this warp's among them
   const int groups = a.warps * (32 / G);                   // heads of a token worked on at once
@@ -166,9 +187,12 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__
             const int p0 = second ? i0 - half : i0;
             weights8(wt, second ? p0 : i0 + half, a.offset, B[v]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              A[v][e] *= cs[p0 + e];
-              B[v][e] *= second ? sn[p0 + e] : -sn[p0 + e];
+            for (int e = 0; e < 8; e += 4) {  // 16-byte aligned: rotary is a multiple of 16
+              const float4 c4 = *reinterpret_cast<const float4*>(cs + p0 + e);
+              const float4 s4 = *reinterpret_cast<const float4*>(sn + p0 + e);
+              const float sg = second ? 1.f : -1.f;
+              A[v][e] *= c4.x, A[v][e + 1] *= c4.y, A[v][e + 2] *= c4.z, A[v][e + 3] *= c4.w;
+              B[v][e] *= sg * s4.x, B[v][e + 1] *= sg * s4.y, B[v][e + 2] *= sg * s4.z, B[v][e + 3] *= sg * s4.w;
             }
           }
         } else if constexpr (PAIRING == NEIGHBOURS) {
@@ -194,6 +218,14 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__
           }
         }
       }
+      uint64_t A2[VPL][4], B2[VPL][4];
+#pragma unroll
+      for (int v = 0; v < VPL; ++v)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          A2[v][q] = pair2(A[v][2 * q], A[v][2 * q + 1]);
+          B2[v][q] = pair2(B[v][2 * q], B[v][2 * q + 1]);
+        }
       for (int h0 = lo + grp; h0 < hi; h0 += kAhead * groups) {
         Raw8<T> raw[kAhead][VPL], other[PAIRING == HALVES && VPL > 1 ? kAhead : 1][VPL];
 #pragma unroll
@@ -215,7 +247,7 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__
           if (h0 + u * groups >= hi) break;
           const int64_t at = (int64_t)(h0 + u * groups - base) * D;
           float f[VPL][8], p[VPL][8];
-          float ss = 0.f;
+          uint64_t sum = 0;
 #pragma unroll
           for (int v = 0; v < VPL; ++v) {
             const int i0 = (lane + v * G) * 8;
@@ -241,21 +273,31 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__
               }
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(f[v][e], f[v][e], ss);
+            for (int q = 0; q < 4; ++q) {
+              const uint64_t x2 = pair2(f[v][2 * q], f[v][2 * q + 1]);
+              sum = fma2(x2, x2, sum);
+            }
           }
+          float ss, odd;
+          split2(sum, ss, odd);
+          ss += odd;
 #pragma unroll
           for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
           // every lane of the group has read the head before any lane writes
           // it (the outputs may be the inputs)
           __syncwarp(mask);
-          const float r = rsqrtf(ss / (float)D + a.eps);
+          const float r = rsqrtf(ss * inv_d + a.eps);
+          const uint64_t r2 = pair2(r, r);
 #pragma unroll
           for (int v = 0; v < VPL; ++v) {
             const int i0 = (lane + v * G) * 8;
             if (i0 >= D) continue;
             float y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = r * fmaf(f[v][e], A[v][e], p[v][e] * B[v][e]);
+            for (int q = 0; q < 4; ++q)
+              split2(mul2(r2, fma2(pair2(f[v][2 * q], f[v][2 * q + 1]), A2[v][q],
+                                   mul2(pair2(p[v][2 * q], p[v][2 * q + 1]), B2[v][q]))),
+                     y[2 * q], y[2 * q + 1]);
             store8(y0 + at + i0, y);
           }
         }

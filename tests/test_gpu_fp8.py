@@ -84,6 +84,25 @@ def test_quantize_rows_is_bit_exact(lib, torch, M, I, dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_nan_signs_and_infinities_at_block_edges(lib, torch, dt):
+    """Every NaN and infinity, either sign, gets the code 0x7f; the block's
+    other values keep the scale of its finite ones."""
+    rng = np.random.default_rng(9)
+    W = oracle.round_to(rng.standard_normal((160, 272)), dt).astype(np.float32)
+    t = dev(W, dt)
+    bits = t.view(torch.int16 if dt == "bf16" else torch.int32)
+    for (r, c), b in (((0, 0), 0x7F81), ((127, 127), 0xFFC0), ((128, 128), 0xFF80), ((159, 271), 0x7F80),
+                      ((5, 255), 0xFFFF)):
+        b = b if dt == "bf16" else b << 16
+        bits[r, c] = b - (1 << 16 if dt == "bf16" else 1 << 32) if b >> (15 if dt == "bf16" else 31) else b
+        W[r, c] = np.nan
+    for enc, ref in ((encode, oracle.fp8_quantize), (encode_rows, oracle.fp8_quantize_rows)):
+        c, s = enc(lib, torch, t)
+        cr, sr = ref(W)
+        assert np.array_equal(s.cpu().numpy(), sr) and np.array_equal(c.cpu().numpy(), cr)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_scale_extremes(lib, torch, dt):
     """Blocks whose largest value is at either end of the type's range, or just
     at and just above 448 times a power of two."""
