@@ -203,20 +203,28 @@ fp8_quantize_kernel(const T* __restrict__ W, int64_t O, int64_t I, uint8_t* __re
 }
 
 // 16 lanes per block of 128 columns of one token, kRowBlocks consecutive
-// blocks of the token in flight per lane.
+// blocks of the token in flight per lane. A CTA's 16 groups of lanes take up to
+// 16 tokens (1 << row_bits) side by side, so that a block's scales, which lie
+// token by token, leave as runs of bytes: with all 16 groups on one token they
+// were single bytes, a sector each.
 constexpr int kRowBlocks = 4;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) fp8_quantize_rows_kernel(const T* __restrict__ X, int64_t M, int64_t I,
-                                                                     uint8_t* __restrict__ codes,
+                                                                     int row_bits, uint8_t* __restrict__ codes,
                                                                      uint8_t* __restrict__ scales) {
+  __shared__ uint8_t bytes[kRowBlocks][kThreads / 16];
   pdl_enter(X);
   const uint32_t nb = (uint32_t)ceil_div(I, kBlock), units = (nb + kRowBlocks - 1) / kRowBlocks;
-  const uint32_t unit = blockIdx.x * (kThreads / 16) + threadIdx.x / 16;  // host: fewer than 2^31
-  const uint32_t m = unit / units, b0 = (unit - m * units) * kRowBlocks;
+  const uint32_t group = threadIdx.x / 16, col_bits = 4 - row_bits;
+  // CTAs walk the columns of a band of tokens first
+  const uint32_t across = (units + (1u << col_bits) - 1) >> col_bits;
+  const uint32_t band = blockIdx.x / across;
+  const uint32_t m = (band << row_bits) + (group & ((1u << row_bits) - 1));
+  const uint32_t b0 = (((blockIdx.x - band * across) << col_bits) + (group >> row_bits)) * kRowBlocks;
   const int lane = threadIdx.x % 16;
   const int64_t at = (int64_t)m * I + (int64_t)b0 * kBlock + lane * 8;
   // this lane's vectors inside the row
-  const int live = m < M ? (int)max((int64_t)0, min((int64_t)kRowBlocks,
+  const int live = m < M && b0 < nb ? (int)max((int64_t)0, min((int64_t)kRowBlocks,
                                                      ceil_div(I - (int64_t)b0 * kBlock - lane * 8, kBlock)))
                          : 0;
   Raw8<T> raw[kRowBlocks];
@@ -245,8 +253,16 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_rows_kernel(const T* __
     const float inv = inverse_scale(byte);
     if (j < live) {
       *reinterpret_cast<uint2*>(codes + at + j * kBlock) = rare ? encode_checked(raw[j], inv) : raw[j].encode(inv);
-      if (lane == 0) scales[(int64_t)(b0 + j) * M + m] = (uint8_t)byte;
     }
+    if (lane == 0) bytes[j][group] = (uint8_t)byte;
+  }
+  __syncthreads();
+  if (threadIdx.x < kRowBlocks * 16) {
+    // the thread of (block, group): tokens of a block are consecutive threads
+    const uint32_t j = threadIdx.x / 16, g = threadIdx.x % 16;
+    const int64_t token = ((int64_t)band << row_bits) + (g & ((1u << row_bits) - 1));
+    const uint32_t b = (((blockIdx.x - band * across) << col_bits) + (g >> row_bits)) * kRowBlocks + j;
+    if (token < M && b < nb) scales[(int64_t)b * M + token] = bytes[j][g];
   }
 }
 
@@ -265,14 +281,15 @@ cudaError_t launch_fp8_quantize(const LaunchCtx& c, theta_dtype dt, const void* 
 
 cudaError_t launch_fp8_quantize_rows(const LaunchCtx& c, theta_dtype dt, const void* X, int64_t M, int64_t I,
                                      void* codes, void* scales) {
-  const int64_t units = M * ceil_div(ceil_div(I, kBlock), kRowBlocks);
-  const dim3 grid((unsigned)ceil_div(units, kThreads / 16));
+  const int row_bits = M >= 16 ? 4 : M >= 8 ? 3 : M >= 4 ? 2 : M >= 2 ? 1 : 0;
+  const int64_t units = ceil_div(ceil_div(I, kBlock), kRowBlocks);
+  const dim3 grid((unsigned)(ceil_div(M, (int64_t)1 << row_bits) * ceil_div(units, (int64_t)16 >> row_bits)));
   auto* q = static_cast<uint8_t*>(codes);
   auto* e = static_cast<uint8_t*>(scales);
   return dt == THETA_BF16 ? launch_pdl(fp8_quantize_rows_kernel<bf16>, grid, dim3(kThreads), 0, c.stream, 1,
-                                       static_cast<const bf16*>(X), M, I, q, e)
+                                       static_cast<const bf16*>(X), M, I, row_bits, q, e)
                           : launch_pdl(fp8_quantize_rows_kernel<float>, grid, dim3(kThreads), 0, c.stream, 1,
-                                       static_cast<const float*>(X), M, I, q, e);
+                                       static_cast<const float*>(X), M, I, row_bits, q, e);
 }
 
 size_t forward_fp8_workspace_bytes(int64_t M, int r) { return forward_fp8_umma_workspace_bytes(M, r); }
