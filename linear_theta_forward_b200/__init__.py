@@ -115,9 +115,15 @@ def _check(status: int, where: str) -> None:
         raise ThetaError(status, where)
 
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _dtype_code(t) -> int:
@@ -148,7 +154,10 @@ def _ptr(t, name: str, *, optional: bool = False) -> int | None:
 def _stream(stream) -> int | None:
     if stream is not None:
         return int(stream) if isinstance(stream, int) else stream.cuda_stream
-    return _torch().cuda.current_stream().cuda_stream
+    # the current stream's handle without a Stream object around it (which
+    # costs 3 us, as much as a launch)
+    torch = _torch()
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ptr_array(tensors, name):
@@ -370,42 +379,46 @@ def theta_linear_forward_nvfp4(X, codes, scales, g, s, U, V, Y, workspace=None, 
            "theta_linear_forward_nvfp4")
 
 
-def _typed(t, name, dtype, shape, device=None):
-    """A CUDA tensor's pointer, after its dtype, shape, layout and device (an
-    ordinal; None: the current one) have been checked."""
-    if t.dtype != dtype or t.shape != shape:
+def _here():
+    """(torch, the current device): what a call looks up once. The calls work on the current device; a pointer of another
+    one would fault there, so _arg and _rows refuse it."""
+    torch = _torch()
+    device = torch.cuda.current_device() if torch.cuda.is_initialized() else -2  # no CUDA tensor can exist yet
+    return torch, device
+
+
+def _arg(t, name, dtype, shape, device):
+    """A CUDA tensor's pointer, after its dtype, shape, layout and device have been checked."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    p = _ptr(t, name)
-    _on_device(t, name, device)
-    return p
-
-
-def _on_device(t, name, device=None):
-    """The calls work on the current device: a pointer of another one would fault there."""
-    now = _torch().cuda.current_device() if device is None else device
-    if t.get_device() != now:
-        raise ValueError(f"{name} is on device {t.get_device()}, the current device is {now}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous (row-major, no padding)")
+    raise ValueError(f"{name} is on device {t.get_device()}, the current device is {device}")
 
 
 def theta_fp8_quantize(W0, codes, scales, stream=None) -> None:
     """Encode W0 [O, I] (bf16 or fp32) in E4M3: codes uint8 [O, I], scales
     uint8 [ceil(O/128), ceil(I/128)], one power of two per 128 x 128 block."""
-    torch = _torch()
-    O, I = W0.shape
-    _check(_load().theta_fp8_quantize(_typed(W0, "W0", W0.dtype, (O, I)), O, I, _dtype_code(W0),
-                                      _typed(codes, "codes", torch.uint8, (O, I)),
-                                      _typed(scales, "scales", torch.uint8, (-(-O // 128), -(-I // 128))),
+    torch, dev = _here()
+    O, I = shape = W0.shape
+    _check(_load().theta_fp8_quantize(_arg(W0, "W0", W0.dtype, shape, dev), O, I, _dtype_code(W0),
+                                      _arg(codes, "codes", torch.uint8, shape, dev),
+                                      _arg(scales, "scales", torch.uint8, (-(-O // 128), -(-I // 128)), dev),
                                       _stream(stream)), "theta_fp8_quantize")
 
 
 def theta_fp8_quantize_rows(X, codes, scales, stream=None) -> None:
     """Encode activations X [M, I] (bf16 or fp32) in E4M3: codes uint8 [M, I],
     scales uint8 [ceil(I/128), M], one power of two per token and 128 columns."""
-    torch = _torch()
-    M, I = X.shape
-    _check(_load().theta_fp8_quantize_rows(_typed(X, "X", X.dtype, (M, I)), M, I, _dtype_code(X),
-                                           _typed(codes, "codes", torch.uint8, (M, I)),
-                                           _typed(scales, "scales", torch.uint8, (-(-I // 128), M)),
+    torch, dev = _here()
+    M, I = shape = X.shape
+    _check(_load().theta_fp8_quantize_rows(_arg(X, "X", X.dtype, shape, dev), M, I, _dtype_code(X),
+                                           _arg(codes, "codes", torch.uint8, shape, dev),
+                                           _arg(scales, "scales", torch.uint8, (-(-I // 128), M), dev),
                                            _stream(stream)), "theta_fp8_quantize_rows")
 
 
@@ -414,35 +427,37 @@ def theta_linear_forward_fp8(X, X_codes, X_scales, codes, scales, s, U, V, Y, wo
     and theta_fp8_quantize wrote. X (bf16) may be None when U and V are.
     workspace: CUDA tensor of at least theta_workspace_size(
     THETA_OP_LINEAR_FORWARD_FP8, ...) bytes (None if 0)."""
-    torch = _torch()
+    torch, dev = _here()
     u8, bf = torch.uint8, torch.bfloat16
-    M, I = X_codes.shape
+    if (U is None) != (V is None):
+        raise ValueError("U and V must be given together")
+    M, I = x_shape = X_codes.shape
     O = codes.shape[0]
     nb = -(-I // 128)
     rank = 0 if U is None else U.shape[1]
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
-        ws_ptr, ws_bytes = _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
-        _on_device(workspace, "workspace")
-    if (U is None) != (V is None):
-        raise ValueError("U and V must be given together")
+        ws_ptr = _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev)
+        ws_bytes = workspace.nbytes
     _check(_load().theta_linear_forward_fp8(
-        None if X is None else _typed(X, "X", bf, (M, I)), _typed(X_codes, "X_codes", u8, (M, I)),
-        _typed(X_scales, "X_scales", u8, (nb, M)), M, I, _typed(codes, "codes", u8, (O, I)),
-        _typed(scales, "scales", u8, (-(-O // 128), nb)), O, _typed(s, "s", torch.float32, (O,)),
-        None if U is None else _typed(U, "U", bf, (O, rank)), None if V is None else _typed(V, "V", bf, (I, rank)),
-        rank, _typed(Y, "Y", bf, (M, O)), ws_ptr, ws_bytes, _stream(stream)), "theta_linear_forward_fp8")
+        None if X is None else _arg(X, "X", bf, x_shape, dev), _arg(X_codes, "X_codes", u8, x_shape, dev),
+        _arg(X_scales, "X_scales", u8, (nb, M), dev), M, I, _arg(codes, "codes", u8, (O, I), dev),
+        _arg(scales, "scales", u8, (-(-O // 128), nb), dev), O, _arg(s, "s", torch.float32, (O,), dev),
+        None if U is None else _arg(U, "U", bf, (O, rank), dev), None if V is None else _arg(V, "V", bf, (I, rank), dev),
+        rank, _arg(Y, "Y", bf, (M, O), dev), ws_ptr, ws_bytes, _stream(stream)), "theta_linear_forward_fp8")
 
 
-def _rows(t, name, M, head_dim, dtype):
+def _rows(t, name, M, head_dim, dtype, device):
     """(pointer, row pitch, heads) of a [M, heads * head_dim] tensor whose rows are dense (the pitch may be larger)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != M or t.shape[1] % head_dim or t.stride(1) != 1:
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on device {t.get_device()}, the current device is {device}" if t.is_cuda
+                         else f"{name} must be a CUDA tensor")
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not dtype or len(shape) != 2 or shape[0] != M or shape[1] % head_dim or stride[1] != 1:
         raise ValueError(f"{name} must be {dtype} [{M}, heads * {head_dim}] with dense rows, got {t.dtype} "
-                         f"{tuple(t.shape)} with strides {t.stride()}")
-    _on_device(t, name)
-    return t.data_ptr(), t.stride(0) if M > 1 else t.shape[1], t.shape[1] // head_dim
+                         f"{tuple(shape)} with strides {stride}")
+    n = shape[1]
+    return t.data_ptr(), stride[0] if M > 1 else n, n // head_dim
 
 
 def theta_qk_norm_rope(Q, K, q_weight, k_weight, positions, inv_freq, Q_out, K_out, head_dim, eps=1e-6,
@@ -452,24 +467,24 @@ def theta_qk_norm_rope(Q, K, q_weight, k_weight, positions, inv_freq, Q_out, K_o
     first 2 * len(inv_freq) values by positions (int64 [M]) * inv_freq (fp32).
     K and K_out, each weight, and positions with inv_freq may be None. Rows
     may be slices of a wider tensor; Q_out and K_out may be Q and K."""
-    torch = _torch()
+    torch, dev = _here()
     head_dim = int(head_dim)
     if head_dim < 1:
         raise ValueError("head_dim must be positive")
     M, dtype = Q.shape[0], Q.dtype
-    q, ldq, nq = _rows(Q, "Q", M, head_dim, dtype)
-    qo, ldqo, nqo = _rows(Q_out, "Q_out", M, head_dim, dtype)
-    k, ldk, nk = (None, 0, 0) if K is None else _rows(K, "K", M, head_dim, dtype)
-    ko, ldko, nko = (None, 0, 0) if K_out is None else _rows(K_out, "K_out", M, head_dim, dtype)
+    q, ldq, nq = _rows(Q, "Q", M, head_dim, dtype, dev)
+    qo, ldqo, nqo = _rows(Q_out, "Q_out", M, head_dim, dtype, dev)
+    k, ldk, nk = (None, 0, 0) if K is None else _rows(K, "K", M, head_dim, dtype, dev)
+    ko, ldko, nko = (None, 0, 0) if K_out is None else _rows(K_out, "K_out", M, head_dim, dtype, dev)
     if nqo != nq or nko != nk:
         raise ValueError("Q_out and K_out must have as many heads as Q and K")
     half = 0 if inv_freq is None else inv_freq.numel()
     _check(_load().theta_qk_norm_rope(
         q, ldq, nq, k, ldk, nk, M, head_dim, _dtype_code(Q),
-        None if q_weight is None else _typed(q_weight, "q_weight", dtype, (head_dim,)),
-        None if k_weight is None else _typed(k_weight, "k_weight", dtype, (head_dim,)), weight_offset, eps,
-        None if positions is None else _typed(positions, "positions", torch.int64, (M,)),
-        None if inv_freq is None else _typed(inv_freq, "inv_freq", torch.float32, (half,)), 2 * half,
+        None if q_weight is None else _arg(q_weight, "q_weight", dtype, (head_dim,), dev),
+        None if k_weight is None else _arg(k_weight, "k_weight", dtype, (head_dim,), dev), weight_offset, eps,
+        None if positions is None else _arg(positions, "positions", torch.int64, (M,), dev),
+        None if inv_freq is None else _arg(inv_freq, "inv_freq", torch.float32, (half,), dev), 2 * half,
         int(interleaved), qo, ldqo, ko, ldko, _stream(stream)), "theta_qk_norm_rope")
 
 
