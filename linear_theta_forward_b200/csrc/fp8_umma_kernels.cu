@@ -43,7 +43,7 @@ constexpr int kBK = 128;               // bytes of K per stage: 128 codes, or 64
 constexpr int kRankBK = 64;
 constexpr int kABytes = kBM * 128;
 constexpr int kGroup = 4;              // K blocks per scale word
-constexpr int kPitch = 129;            // fp32 pitch of the split-K partial tiles
+constexpr int kPitch = 132;            // fp32 pitch of the split-K partial tiles (16-byte rows)
 
 struct Args {
   int rows;   // O
@@ -308,16 +308,18 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     ptx::cluster_sync();  // every CTA of the cluster has staged its partial tile
     if (!*abort_flag) {
       const int col0 = n_tile * BN;
-      const int E = min(BN, args.cols - col0) * kBM;
+      // four rows at a time: O is a multiple of 8, so they are all inside or all outside
+      const int E = min(BN, args.cols - col0) * (kBM / 4);
       const int e0 = (int)((int64_t)split * E / args.splits), e1 = (int)((int64_t)(split + 1) * E / args.splits);
       const uint32_t part_addr = ptx::smem_u32(smem);
+#pragma unroll 2
       for (int e = e0 + threadIdx.x; e < e1; e += kThreads) {
-        const int c = e / kBM, rr = e % kBM;
-        const uint32_t off = part_addr + (uint32_t)((c * kPitch + rr) * 4);
-        float v = 0.f;
-        for (int p = 0; p < args.splits; ++p) v += ptx::ld_dsmem_f32(ptx::mapa(off, (uint32_t)p));
+        const int c = e / (kBM / 4), rr = e % (kBM / 4) * 4;
         const int grow = m_tile * kBM + rr;
-        if (grow < args.rows) args.out[(int64_t)(col0 + c) * args.rows + grow] = __float2bfloat16_rn(v);
+        if (grow >= args.rows) continue;
+        const float4 v = ptx::cluster_sum4(part_addr + (uint32_t)((c * kPitch + rr) * 4), args.splits);
+        *reinterpret_cast<uint2*>(args.out + (int64_t)(col0 + c) * args.rows + grow) =
+            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
       }
     }
     ptx::cluster_sync();  // no CTA leaves while a peer still reads its tile

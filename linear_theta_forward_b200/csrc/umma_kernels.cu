@@ -351,17 +351,15 @@ umma_kernel(const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CU
       for (int e = e0 + threadIdx.x; e < e1; e += kThreads) {
         const int c = e / kBM, rr = e % kBM;
         const uint32_t off = part_addr + (uint32_t)((c * kPitch + rr) * 4);
-        float v = 0.f;
-        for (int p = 0; p < args.splits; ++p) v += ptx::ld_dsmem_f32(ptx::mapa(off, (uint32_t)p));
         const int grow = m_tile * kBM + rr;
         if (grow >= args.rows) continue;
+        const float v = ptx::cluster_sum(off, args.splits);
         if constexpr (MODE == MODE_FORWARD) {
           args.out[(int64_t)(col0 + c) * args.rows + grow] = __float2bfloat16_rn(v);
         } else if constexpr (MODE == MODE_GATE_UP) {
           // v is the gate pre-activation; the up one is the tile BN columns further
           const uint32_t off_u = off + (uint32_t)(BN * kPitch * 4);
-          float u = 0.f;
-          for (int p = 0; p < args.splits; ++p) u += ptx::ld_dsmem_f32(ptx::mapa(off_u, (uint32_t)p));
+          const float u = ptx::cluster_sum(off_u, args.splits);
           args.out[(int64_t)(col0 + c) * args.rows + grow] = __float2bfloat16_rn(gelu_tanh(v) * u);
         } else if constexpr (MODE == MODE_XV) {
           const int j = col0 + c;

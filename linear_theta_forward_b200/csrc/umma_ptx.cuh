@@ -362,5 +362,45 @@ __device__ __forceinline__ float ld_dsmem_f32(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ float4 ld_dsmem_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// The sum over the cluster's first n CTAs (n <= 16), in their order, of the
+// float at this shared-memory address in each. All loads are issued before
+// the first addition: one remote latency instead of n.
+constexpr int kMaxCluster = 16;
+__device__ __forceinline__ float cluster_sum(uint32_t addr, int n) {
+  float x[kMaxCluster];
+#pragma unroll
+  for (int p = 0; p < kMaxCluster; ++p)
+    if (p < n) x[p] = ld_dsmem_f32(mapa(addr, (uint32_t)p));
+  float v = 0.f;
+#pragma unroll
+  for (int p = 0; p < kMaxCluster; ++p)
+    if (p < n) v += x[p];
+  return v;
+}
+// The same for four neighbouring floats (16-byte aligned), kept to four
+// loads in flight.
+__device__ __forceinline__ float4 cluster_sum4(uint32_t addr, int n) {
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p0 = 0; p0 < n; p0 += 4) {
+    float4 x[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+      if (p0 + p < n) x[p] = ld_dsmem_f32x4(mapa(addr, (uint32_t)(p0 + p)));
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+      if (p0 + p < n) v.x += x[p].x, v.y += x[p].y, v.z += x[p].z, v.w += x[p].w;
+  }
+  return v;
+}
+
 }  // namespace ptx
 }  // namespace theta
