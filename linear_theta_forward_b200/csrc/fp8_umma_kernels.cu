@@ -56,6 +56,7 @@ struct Args {
   const float* s;
   bf16* out;
   int early_start;  // launched right after this call's T = X.V kernel
+  int tile_tokens;  // CTA pairs: tokens of a tile, a multiple of 16, at most kPairN
   unsigned* err;
 };
 
@@ -91,7 +92,7 @@ struct Cfg {
   static constexpr int kSf = 2 * BN;                       // first scale column (after D1, D2); 8 per group
   static constexpr int kTmemNeed = kSf + 8 * kRing;
   static constexpr int kTmemCols = kTmemNeed <= 64 ? 64 : kTmemNeed <= 128 ? 128 : kTmemNeed <= 256 ? 256 : 512;
-  static_assert(kTmemNeed <= 512 && kSfbCols <= 4, "accumulators and scales must fit in tensor memory");
+  static_assert(kTmemNeed <= 512 && kSfbCols <= 4 && BN <= 64, "accumulators and scales must fit in tensor memory");
   static_assert(BN * kPitch * 4 <= kStages * kStageBytes, "partial tile must fit in the stage ring");
   static constexpr int kSmemBytes = kStages * kStageBytes + 1024 /*align*/ + 256 /*barriers*/;
 };
@@ -259,12 +260,8 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
       ptx::tc_fence_after();
       const uint32_t sf = tmem + lanes + (uint32_t)(C::kSf + 8 * ring);
       ptx::tmem_st4(sf, wa[0], wa[0], wa[0], wa[0]);
-      if constexpr (C::kSfbCols == 4) {
-        ptx::tmem_st4(sf + 4, wb[0], wb[1], wb[2], wb[3]);
-      } else {
 #pragma unroll
-        for (int c = 0; c < C::kSfbCols; ++c) ptx::tmem_st1(sf + 4 + c, wb[c]);
-      }
+      for (int c = 0; c < C::kSfbCols; ++c) ptx::tmem_st1(sf + 4 + c, wb[c]);
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
       __syncwarp();
@@ -331,7 +328,8 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
 }
 
 // ------------------------------------------------------------ CTA-pair tiles
-// 256 rows x up to 240 tokens per pair of SMs (cta_group::2), persistent. Each
+// 256 rows x up to 240 tokens (tile_tokens, the tokens spread evenly over the
+// fewest tiles) per pair of SMs (cta_group::2), persistent. Each
 // CTA stages 128 rows of W0 codes and half of the tile's tokens per K block
 // and holds its 128 rows of both accumulators. 240 tokens, not 256: D1 and D2
 // take 2 x 240 columns of tensor memory and the scales of two groups the
@@ -382,14 +380,16 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t cta = ptx::cluster_ctarank();  // 0 issues the MMAs
   const int cluster = blockIdx.x / 2, n_clusters = gridDim.x / 2;
-  const int n_tiles = (args.cols + kPairN - 1) / kPairN;
+  const int width = args.tile_tokens;
+  const int n_tiles = (args.cols + width - 1) / width;
   const int tiles = n_tiles * ((args.rows + 2 * kBM - 1) / (2 * kBM));
   const bool has_d2 = args.kb2 > 0;
   const int n1 = args.kb1;
   const int per_tile = n1 + (has_d2 ? 2 * args.kb2 : 0);
   const int groups = (n1 + kGroup - 1) / kGroup;
   // tokens of a tile's MMA: the last tile's rounded up to a multiple of 16
-  auto tile_n = [&](int tile) { return min(kPairN, (args.cols - (tile % n_tiles) * kPairN + 15) / 16 * 16); };
+  auto tile_n = [&](int tile) { return min(width, (args.cols - (tile % n_tiles) * width + 15) / 16 * 16); };
+  const uint32_t stage_bytes = kABytes + width / 2 * 128;  // that a CTA loads per stage
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
@@ -432,7 +432,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     int g = 0;  // stage items issued, over all tiles
     for (int tile = cluster; tile < tiles && !stop; tile += n_clusters) {
       const int row0 = (tile / n_tiles) * (2 * kBM) + (int)cta * kBM;
-      const int tok0 = (tile % n_tiles) * kPairN + (int)cta * (tile_n(tile) / 2);
+      const int tok0 = (tile % n_tiles) * width + (int)cta * (tile_n(tile) / 2);
       for (int i = 0; i < per_tile; ++i, ++g) {
         const int st = g % S;
         if (!ptx::mbar_wait(&empty[st], ((uint32_t)(g / S) & 1u) ^ 1u, abort_flag)) {
@@ -443,7 +443,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         uint8_t* a = smem + st * kPairStageBytes;
         uint8_t* b = a + kABytes;
         const uint32_t bar = full0 + (uint32_t)(st * 8);
-        if (cta == 0) ptx::mbar_arrive_expect_tx(&full[st], 2 * kPairStageBytes);  // both CTAs' loads
+        if (cta == 0) ptx::mbar_arrive_expect_tx(&full[st], 2 * stage_bytes);  // both CTAs' loads
         if (i < n1) {
           ptx::tma_load_2d_pair(a, &tmW, bar, i * kBK, row0);
           ptx::tma_load_2d_pair(b, &tmX, bar, i * kBK, tok0);
@@ -549,7 +549,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
       // the odd CTA's rows may all be past O: its scales are then not used
       const int rb = min((tile / n_tiles) * 2 + (int)cta, row_blocks - 1);
       const uint8_t* wsp = args.ws + (int64_t)rb * args.kb1;
-      const int tok = (tile % n_tiles) * kPairN + lane;
+      const int tok = (tile % n_tiles) * width + lane;
       for (int q = 0; q < groups; ++q, ++sg) {
         if ((sg & 1) != (warp & 1)) continue;
         const int ring = sg % kPairRing, kb = q * kGroup;
@@ -585,8 +585,8 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     int j = 0;
     for (int tile = cluster; tile < tiles; tile += n_clusters, ++j) {
       const int row0 = (tile / n_tiles) * (2 * kBM) + (int)cta * kBM;
-      const int col0 = (tile % n_tiles) * kPairN;
-      const int ncols = min(kPairN, args.cols - col0) - part * 128;  // of this warp's columns
+      const int col0 = (tile % n_tiles) * width;
+      const int ncols = min(width, args.cols - col0) - part * 128;  // of this warp's columns
       const int grow = row0 + row;
       const float so = grow < args.rows ? args.s[grow] : 0.f;
       const bool got = __all_sync(0xffffffffu, ptx::mbar_wait(accum, (uint32_t)j & 1u, abort_flag));
@@ -650,6 +650,18 @@ struct Maps {
   CUtensorMap w, x, u, th, tl;
 };
 
+// K splits of the one-SM tiles: while every SM still gets at most one CTA and
+// each split keeps 8 K blocks; below that the sum over the cluster costs more
+// than the shorter walk saves (128 tokens of [1152, 6912], 54 blocks: 23.2 us
+// unsplit, 16.1, 12.0 and 14.7 with 2, 4 and 8 splits; one token of [6912,
+// 1152], 9 blocks: 8.7 and 9.3 with 1 and 2).
+int tile_splits(const LaunchCtx& c, int64_t m_tiles, int64_t n_tiles, int kb) {
+  int s = 1;
+  if (c.policy != THETA_POLICY_THROUGHPUT)
+    while (s < 8 && m_tiles * n_tiles * 2 * s <= c.num_sms && kb / (2 * s) >= 8) s *= 2;
+  return s;
+}
+
 template <int BN>
 cudaError_t launch_tile(const LaunchCtx& c, const Maps& mp, Args args) {
   using C = Cfg<BN>;
@@ -658,11 +670,7 @@ cudaError_t launch_tile(const LaunchCtx& c, const Maps& mp, Args args) {
   cudaError_t e = prepare_kernel(&info[c.device], c.device, kern, kThreads, C::kSmemBytes, C::kTmemCols, true);
   if (e != cudaSuccess) return e;
   const int m_tiles = (int)ceil_div(args.rows, kBM), n_tiles = (int)ceil_div(args.cols, BN);
-  // as in the bf16 forward: tiles of 64 or more tokens count one CTA per SM
-  const int capacity = c.num_sms * (BN >= 64 ? 1 : info[c.device].blocks_per_sm);
-  args.splits = c.policy == THETA_POLICY_THROUGHPUT
-                    ? 1
-                    : pick_splits((int64_t)m_tiles * n_tiles, args.kb1, capacity, info[c.device].max_cluster);
+  args.splits = tile_splits(c, m_tiles, n_tiles, args.kb1);
   return launch_pdl(kern, dim3((unsigned)(n_tiles * args.splits), (unsigned)m_tiles), dim3(kThreads), C::kSmemBytes,
                     c.stream, args.splits, mp.w, mp.x, mp.u, mp.th, mp.tl, args);
 }
@@ -672,7 +680,7 @@ cudaError_t launch_pair(const LaunchCtx& c, const Maps& mp, const Args& args, co
   cudaError_t e =
       prepare_kernel(&info[c.device], c.device, fp8_pair_kernel, kPairThreads, kPairSmemBytes, 512, false);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = ceil_div(args.rows, 2 * kBM) * ceil_div(args.cols, kPairN);
+  const int64_t tiles = ceil_div(args.rows, 2 * kBM) * ceil_div(args.cols, args.tile_tokens);
   const int64_t clusters = tiles < c.num_sms / 2 ? tiles : c.num_sms / 2;  // one CTA per SM
   return launch_pdl(fp8_pair_kernel, dim3((unsigned)(2 * clusters)), dim3(kPairThreads), kPairSmemBytes, c.stream, 2,
                     mp.w, mp.x, mp.u, mp.th, mp.tl, mY, args);
@@ -696,12 +704,16 @@ int launch_forward_fp8_umma(const LaunchCtx& c, const void* X, const void* xq, c
     t_lo = reinterpret_cast<bf16*>(static_cast<uint8_t*>(work) + forward_fp8_umma_workspace_bytes(M, r) / 2);
     if ((st = launch_xv_umma(c, X, V, M, I, r, t_hi, t_lo, ce))) return st;
   }
-  const int m_tiles = (int)ceil_div(O, kBM);
-  // Pairs when they fill the GPU, or when every CTA takes a whole tile anyway
-  const bool pair =
-      M > 128 && (c.policy == THETA_POLICY_THROUGHPUT || m_tiles * ceil_div(M, kPairN) >= (int64_t)c.num_sms);
-  const int BN = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-  const int box = pair ? kPairHalf : BN;  // tokens per box
+  const int width = (int)(ceil_div(ceil_div(M, ceil_div(M, kPairN)), 16) * 16);  // tokens of a pair's tile
+  // 64 tokens a tile at most on one SM: wider tiles leave SMs without work or
+  // cost splits (333 tokens of [2056, 1168]: 13.2 us against 16.3 with 128)
+  const int BN = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+  // More than 64 tokens: CTA pairs, which load less per product, unless the
+  // one-SM tiles are so few that they split K (us, one-SM and pairs: 2048
+  // tokens of [21504, 5376] 424 and 254; 128 tokens of [8192, 5376] 22.7 and
+  // 22.0; 100 tokens of [1152, 6912] 11.6 and 22.9).
+  const bool pair = M > 64 && tile_splits(c, ceil_div(O, kBM), ceil_div(M, 64), (int)ceil_div(I, kBK)) == 1;
+  const int box = pair ? width / 2 : BN;  // tokens per box
   Maps mp;
   if ((st = make_map_box(&mp.w, wq, O, I, kBM, kBK, CU_TENSOR_MAP_SWIZZLE_128B, ce, 1))) return st;
   if ((st = make_map_box(&mp.x, xq, M, I, box, kBK, CU_TENSOR_MAP_SWIZZLE_128B, ce, 1))) return st;
@@ -723,17 +735,17 @@ int launch_forward_fp8_umma(const LaunchCtx& c, const void* X, const void* xq, c
   a.s = s;
   a.out = static_cast<bf16*>(Y);
   a.early_start = r > 0;
+  a.tile_tokens = width;
   a.err = c.err;
   if (pair) {
     CUtensorMap mY;
-    if ((st = make_map_box(&mY, Y, M, O, kPairN, kBM, CU_TENSOR_MAP_SWIZZLE_NONE, ce))) return st;
+    if ((st = make_map_box(&mY, Y, M, O, width, kBM, CU_TENSOR_MAP_SWIZZLE_NONE, ce))) return st;
     *ce = launch_pair(c, mp, a, mY);
   } else {
     switch (BN) {
       case 16: *ce = launch_tile<16>(c, mp, a); break;
       case 32: *ce = launch_tile<32>(c, mp, a); break;
-      case 64: *ce = launch_tile<64>(c, mp, a); break;
-      default: *ce = launch_tile<128>(c, mp, a); break;
+      default: *ce = launch_tile<64>(c, mp, a); break;
     }
   }
   return *ce == cudaSuccess ? THETA_OK : THETA_ERR_CUDA;
