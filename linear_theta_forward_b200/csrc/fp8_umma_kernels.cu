@@ -27,6 +27,7 @@
 // Waits are bounded as everywhere in the library.
 #include <cuda.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "common.cuh"
@@ -56,6 +57,9 @@ struct Args {
   const float* s;
   bf16* out;
   int early_start;  // launched right after this call's T = X.V kernel
+  const float* t_parts;  // few tokens: [nparts, cols, r] partial sums of T = X.V
+  const bf16* U;
+  int nparts, r;
   int tile_tokens;  // CTA pairs: tokens of a tile, a multiple of 16, at most kPairN
   unsigned* err;
 };
@@ -82,6 +86,14 @@ __device__ __forceinline__ void scale_words(const uint8_t* p, int64_t pitch, int
 // ------------------------------------------------------------ one-SM tiles
 constexpr int kThreads = 192;
 
+// One or two tokens (FEW): T = X.V comes as fp32 partial sums from a CUDA-core
+// kernel, and the rank term is a dot product of at most 256 values per row in
+// the epilogue -- shorter than a tensor-core T and two more accumulations (one
+// token of [6912, 1152], rank 32: 5.1 us without a rank term, 7.9 us with T
+// on tensor cores).
+constexpr int kFewTokens = 2;
+constexpr int kMaxRank = 256;
+
 template <int BN>
 struct Cfg {
   static constexpr int kBBytes = BN * 128;
@@ -97,7 +109,7 @@ struct Cfg {
   static constexpr int kSmemBytes = kStages * kStageBytes + 1024 /*align*/ + 256 /*barriers*/;
 };
 
-template <int BN>
+template <int BN, bool FEW>
 __global__ void __launch_bounds__(kThreads)
 fp8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                 const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmTh,
@@ -271,6 +283,33 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     const int row = quarter * 32 + lane;  // accumulator row = tensor-memory lane
     const uint32_t taddr = tmem + lanes;
     if (early) asm volatile("griddepcontrol.wait;" ::: "memory");
+    float rank_term[kFewTokens] = {};
+    if constexpr (FEW) {
+      if (split == 0 && args.r > 0) {
+        __shared__ float t_sum[kFewTokens * kMaxRank];  // [token][r]
+        const int n = args.cols * args.r;
+        for (int i = threadIdx.x - 64; i < n; i += 128) {
+          float t = 0.f;
+#pragma unroll 8
+          for (int p = 0; p < args.nparts; ++p) t += args.t_parts[p * n + i];
+          t_sum[i] = t;
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (m_tile * kBM + row < args.rows) {
+          const uint4* u = reinterpret_cast<const uint4*>(args.U + (int64_t)(m_tile * kBM + row) * args.r);
+#pragma unroll 4
+          for (int j = 0; j < args.r / 8; ++j) {
+            float f[8];
+            unpack(u[j], f);
+#pragma unroll
+            for (int m = 0; m < kFewTokens; ++m)
+              if (m < args.cols)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) rank_term[m] = fmaf(f[e], t_sum[m * args.r + 8 * j + e], rank_term[m]);
+          }
+        }
+      }
+    }
     bool ok = ptx::mbar_wait(accum, 0, abort_flag);
     if (!ok) give_up();
     ok = __all_sync(0xffffffffu, ok);  // tcgen05.ld below is warp-collective
@@ -288,7 +327,11 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         ptx::tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float v = has_d2 ? fmaf(so, d1[e], d2[e]) : so * d1[e];
+          float v = has_d2 ? fmaf(so, d1[e], d2[e]) : so * d1[e];
+          if constexpr (FEW) {
+            if (e >= kFewTokens) break;
+            v = fmaf(so, d1[e], rank_term[e]);
+          }
           const int m = col0 + c0 + e;
           if (args.splits > 1)
             part[(c0 + e) * kPitch + row] = v;
@@ -662,10 +705,10 @@ int tile_splits(const LaunchCtx& c, int64_t m_tiles, int64_t n_tiles, int kb) {
   return s;
 }
 
-template <int BN>
+template <int BN, bool FEW = false>
 cudaError_t launch_tile(const LaunchCtx& c, const Maps& mp, Args args) {
   using C = Cfg<BN>;
-  auto kern = fp8_tile_kernel<BN>;
+  auto kern = fp8_tile_kernel<BN, FEW>;
   static KernelInfo info[64];
   cudaError_t e = prepare_kernel(&info[c.device], c.device, kern, kThreads, C::kSmemBytes, C::kTmemCols, true);
   if (e != cudaSuccess) return e;
@@ -688,9 +731,14 @@ cudaError_t launch_pair(const LaunchCtx& c, const Maps& mp, const Args& args, co
 
 }  // namespace
 
+// Slices of I in the partial sums of T = X.V: about 84 rows of V each, up to 64.
+constexpr int kXvParts = 64;
+constexpr int kXvRows = 84;
+
 size_t forward_fp8_umma_workspace_bytes(int64_t M, int r) {
   const size_t half = ((size_t)M * r * 2 + 255) / 256 * 256;
-  return 2 * half;  // T's high and low parts
+  const size_t parts = M <= kFewTokens ? (size_t)kXvParts * M * r * sizeof(float) : 0;
+  return std::max(2 * half, parts);  // T's high and low parts, or its partial sums
 }
 
 int launch_forward_fp8_umma(const LaunchCtx& c, const void* X, const void* xq, const void* xs, const void* wq,
@@ -700,7 +748,12 @@ int launch_forward_fp8_umma(const LaunchCtx& c, const void* X, const void* xq, c
   int st;
   bf16* t_hi = static_cast<bf16*>(work);
   bf16* t_lo = nullptr;
-  if (r > 0) {
+  const bool few = M <= kFewTokens;
+  const int nparts = (int)std::min<int64_t>(kXvParts, ceil_div(I, kXvRows));
+  if (few && r > 0) {
+    *ce = launch_xv_parts(c, X, V, M, I, r, nparts, static_cast<float*>(work));
+    if (*ce != cudaSuccess) return THETA_ERR_CUDA;
+  } else if (r > 0) {
     t_lo = reinterpret_cast<bf16*>(static_cast<uint8_t*>(work) + forward_fp8_umma_workspace_bytes(M, r) / 2);
     if ((st = launch_xv_umma(c, X, V, M, I, r, t_hi, t_lo, ce))) return st;
   }
@@ -719,7 +772,7 @@ int launch_forward_fp8_umma(const LaunchCtx& c, const void* X, const void* xq, c
   if ((st = make_map_box(&mp.x, xq, M, I, box, kBK, CU_TENSOR_MAP_SWIZZLE_128B, ce, 1))) return st;
   mp.u = mp.w;
   mp.th = mp.tl = mp.x;
-  if (r > 0) {
+  if (r > 0 && !few) {
     if ((st = make_map_box(&mp.u, U, O, r, kBM, kRankBK, CU_TENSOR_MAP_SWIZZLE_128B, ce))) return st;
     if ((st = make_map_box(&mp.th, t_hi, M, r, box, kRankBK, CU_TENSOR_MAP_SWIZZLE_128B, ce))) return st;
     if ((st = make_map_box(&mp.tl, t_lo, M, r, box, kRankBK, CU_TENSOR_MAP_SWIZZLE_128B, ce))) return st;
@@ -728,10 +781,14 @@ int launch_forward_fp8_umma(const LaunchCtx& c, const void* X, const void* xq, c
   a.rows = (int)O;
   a.cols = (int)M;
   a.kb1 = (int)ceil_div(I, kBK);
-  a.kb2 = (int)ceil_div(r, kRankBK);
+  a.kb2 = few ? 0 : (int)ceil_div(r, kRankBK);
   a.splits = 1;
   a.xs = static_cast<const uint8_t*>(xs);
   a.ws = static_cast<const uint8_t*>(ws);
+  a.t_parts = static_cast<const float*>(work);
+  a.U = static_cast<const bf16*>(U);
+  a.nparts = nparts;
+  a.r = r;
   a.s = s;
   a.out = static_cast<bf16*>(Y);
   a.early_start = r > 0;
@@ -743,7 +800,7 @@ int launch_forward_fp8_umma(const LaunchCtx& c, const void* X, const void* xq, c
     *ce = launch_pair(c, mp, a, mY);
   } else {
     switch (BN) {
-      case 16: *ce = launch_tile<16>(c, mp, a); break;
+      case 16: *ce = few ? launch_tile<16, true>(c, mp, a) : launch_tile<16>(c, mp, a); break;
       case 32: *ce = launch_tile<32>(c, mp, a); break;
       default: *ce = launch_tile<64>(c, mp, a); break;
     }

@@ -626,6 +626,13 @@ cudaError_t launch_m(const LaunchCtx& c, GemvArgs a, const void* V) {
 
 }  // namespace
 
+cudaError_t launch_xv_parts(const LaunchCtx& c, const void* X, const void* V, int64_t M, int64_t I, int r, int nparts,
+                            float* parts) {
+  auto kern = M == 1 ? xv_parts_kernel<1> : xv_parts_kernel<2>;
+  return launch_pdl(kern, dim3((unsigned)nparts), dim3(kThreads), 0, c.stream, 1, static_cast<const bf16*>(X),
+                    static_cast<const bf16*>(V), I, r, parts);
+}
+
 int forward_gemv_max_tokens() { return kMaxTokens; }
 
 size_t forward_gemv_workspace_bytes(int64_t M, int r) {

@@ -73,6 +73,11 @@ bool launch_forward_gemv(const LaunchCtx& c, const void* X, const void* W0, cons
                          const void* V, int64_t M, int64_t O, int64_t I, int r, void* Y, void* ws,
                          cudaError_t* e);
 
+// T = X.V of one or two tokens as nparts partial sums over slices of I:
+// parts [nparts, M, r] fp32; r a multiple of 8, at most 256.
+cudaError_t launch_xv_parts(const LaunchCtx& c, const void* X, const void* V, int64_t M, int64_t I, int r, int nparts,
+                            float* parts);
+
 // ---- NVFP4 shared block (gemv_kernels.cu): encode W0 [O, I] bf16 into E2M1
 // codes [O, I/2], E4M3 block scales [O, I/16] and the tensor scale *g (ws: 4
 // bytes of scratch); the forward for one or two tokens from that encoding
