@@ -202,12 +202,35 @@ fp8_quantize_kernel(const T* __restrict__ W, int64_t O, int64_t I, uint8_t* __re
   if (threadIdx.x == 0) scales[bo * nb + bi] = (uint8_t)byte;
 }
 
+// The largest magnitudes of two blocks over 16 lanes: for bf16 both in the
+// halves of one word.
+__device__ __forceinline__ void group_max(const Raw8<bf16>& a, const Raw8<bf16>& b, float& ma, float& mb) {
+  __nv_bfloat162 x = Raw8<bf16>::max_init(), y = x;
+  a.abs_max(x);
+  b.abs_max(y);
+  __nv_bfloat162 m = __hmax2(__lows2bfloat162(x, y), __highs2bfloat162(x, y));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = __hmax2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  ma = __low2float(m);
+  mb = __high2float(m);
+}
+__device__ __forceinline__ void group_max(const Raw8<float>& a, const Raw8<float>& b, float& ma, float& mb) {
+  ma = mb = 0.f;
+  a.abs_max(ma);
+  b.abs_max(mb);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
+    mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+  }
+}
+
 // 16 lanes per block of 128 columns of one token, kRowBlocks consecutive
 // blocks of the token in flight per lane. A CTA's 16 groups of lanes take up to
 // 16 tokens (1 << row_bits) side by side, so that a block's scales, which lie
 // token by token, leave as runs of bytes: with all 16 groups on one token they
 // were single bytes, a sector each.
-constexpr int kRowBlocks = 4;
+constexpr int kRowBlocks = 2;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) fp8_quantize_rows_kernel(const T* __restrict__ X, int64_t M, int64_t I,
                                                                      int row_bits, uint8_t* __restrict__ codes,
@@ -235,13 +258,11 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_rows_kernel(const T* __
     else
       raw[j].zero();
   }
+  float top[kRowBlocks];
+  group_max(raw[0], raw[1], top[0], top[1]);
 #pragma unroll
   for (int j = 0; j < kRowBlocks; ++j) {
-    auto mp = Raw8<T>::max_init();
-    raw[j].abs_max(mp);
-    float mx = Raw8<T>::max_value(mp);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    float mx = top[j];
     const bool rare = mx > kMaxFinite;  // the same in the block's 16 lanes
     if (__any_sync(0xffffffffu, rare)) {
       float fm = finite_abs_max(raw[j], 0.f);
