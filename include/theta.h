@@ -414,7 +414,13 @@ int theta_fp8_quantize_rows(const void* X, int64_t M, int64_t I, theta_dtype dt,
  * theta_fp8_quantize_rows), for any number of tokens:
  *   Y = s (.) (Xq . W0q^T) + (X . V) . U^T
  * with Xq and W0q the values that the codes stand for. The rank-r correction
- * is formed from the bf16 X, so it keeps its precision.
+ * is formed from the bf16 X, so it keeps its precision. Tensor cores apply the
+ * scales (tcgen05 kind::mxf8f6f4, fp32 accumulation in tensor memory): tiles
+ * of 128 rows and up to 64 tokens, K split over a cluster where they are few
+ * (THETA_POLICY_LATENCY), and persistent CTA pairs for more tokens. T = X . V
+ * is a bf16 high and low part as in theta_linear_forward, fp32 for one or two
+ * tokens. A NaN code makes its token's (or its row's) outputs NaN and leaves
+ * the others alone.
  *
  *   X [M, I] bf16 (read for the rank-r term only; may be NULL when rank == 0);
  *   X_codes, X_scales, codes, scales as the two encoders write them; s fp32
@@ -457,7 +463,8 @@ int theta_linear_forward_fp8(const void* X, const void* X_codes, const void* X_s
  *      own input (same pointer, same pitch); any other overlap is not allowed.
  *   1 <= M <= 2^30; D a multiple of 8, at most 1024; rotary_dim even, 0 ..
  *   D; q_heads, k_heads <= 65535; pitches at least the row (M > 1) and
- *   multiples of 8; base pointers 16-byte aligned; eps >= 0.
+ *   multiples of 8; Q, K, Q_out, K_out and the weights 16-byte aligned;
+ *   eps >= 0.
  */
 int theta_qk_norm_rope(const void* Q, int64_t ldq, int q_heads, const void* K, int64_t ldk, int k_heads, int64_t M,
                        int head_dim, theta_dtype dt, const void* q_weight, const void* k_weight, float weight_offset,

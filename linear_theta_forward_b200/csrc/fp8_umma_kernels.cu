@@ -317,7 +317,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     const int grow = m_tile * kBM + row;
     const int col0 = n_tile * BN;
     const int ncols = min(BN, args.cols - col0);
-    const float so = grow < args.rows ? __ldg(args.s + grow) : 0.f;
+    const float so = grow < args.rows ? args.s[grow] : 0.f;
     float* part = reinterpret_cast<float*>(smem);
     if (ok) {
       for (int c0 = 0; c0 < ncols; c0 += 16) {

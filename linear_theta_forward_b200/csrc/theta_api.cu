@@ -622,9 +622,9 @@ THETA_API int theta_qk_norm_rope(const void* Q, int64_t ldq, int q_heads, const 
                   (long long)row);
     if (h.x == h.y && M > 1 && h.ld != h.ld_out)
       return fail(THETA_ERR_INVALID_ARG, "theta_qk_norm_rope: in place needs equal pitches");
-    if (!aligned16(h.x) || !aligned16(h.y) || h.ld % 8 || h.ld_out % 8)
+    if (!aligned16(h.x) || !aligned16(h.y) || !aligned16(h.weight) || h.ld % 8 || h.ld_out % 8)
       return fail(THETA_ERR_ALIGNMENT,
-                  "theta_qk_norm_rope: Q, K, Q_out, K_out 16-byte aligned, pitches multiples of 8");
+                  "theta_qk_norm_rope: Q, K, Q_out, K_out and the weights 16-byte aligned, pitches multiples of 8");
   }
   if (rotary_dim > 0 &&
       ((reinterpret_cast<uintptr_t>(positions) & 7u) != 0 || (reinterpret_cast<uintptr_t>(inv_freq) & 3u) != 0))

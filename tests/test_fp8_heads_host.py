@@ -118,7 +118,7 @@ def test_heads_refusals(lib):
                 dict(ldq=504), dict(ldqo=504), dict(ldk=248), dict(ldko=0), dict(ldqo=520), dict(ldko=264)):
         assert call(**bad) == -1, bad
     assert call(D=1032, rot=0, ldq=4096, ldqo=4096, ldk=4096, ldko=4096) == -2
-    for bad in (dict(Q=ODD), dict(Qo=ODD), dict(K=ODD), dict(Ko=ODD), dict(ldq=516, ldqo=516), dict(pos=ODD),
+    for bad in (dict(wq=ODD), dict(wk=ODD), dict(Q=ODD), dict(Qo=ODD), dict(K=ODD), dict(Ko=ODD), dict(ldq=516, ldqo=516), dict(pos=ODD),
                 dict(f=ctypes.c_void_p(4098))):
         assert call(**bad) == -3, bad
 

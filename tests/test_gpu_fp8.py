@@ -165,7 +165,7 @@ class Problem:
         assert (self.guard[:256] == 7).all() and (self.guard[256 + M * O:] == 7).all(), "wrote outside Y"
 
 
-SHAPES = [(1, 8, 16, 0), (1, 256, 1152, 32), (1, 1032, 640, 8), (2, 392, 336, 24), (3, 136, 144, 16), (1, 6912, 1152, 0),
+SHAPES = [(1, 8, 16, 0), (1, 256, 1152, 32), (1, 1032, 640, 8), (2, 392, 336, 24), (2, 264, 400, 256), (1, 136, 16, 200), (3, 136, 144, 16), (1, 6912, 1152, 0),
           (5, 128, 128, 8), (8, 264, 4096, 64), (15, 1024, 1152, 40), (16, 2048, 5376, 64), (17, 128, 2064, 0),
           (31, 520, 1296, 256), (33, 776, 272, 32), (64, 1152, 6912, 32), (65, 136, 512, 128), (100, 1000, 1168, 24),
           (128, 256, 1152, 0), (129, 384, 256, 8), (200, 2056, 1168, 24), (256, 1024, 1152, 64), (257, 264, 656, 16),
@@ -289,6 +289,45 @@ def test_captured_and_replayed_and_on_another_stream(lib, torch, M):
         g.replay()
         lib.theta_device_status()
         p.check(what=f"replay {k}")
+
+
+@pytest.mark.parametrize("M", [1, 16, 300])
+def test_work_after_a_timeout_is_flagged_then_recovers(lib, torch, M):
+    """A forward enqueued while the timeout flag is set gives up within its
+    bounded waits; the next one, after the flag has been read, is right."""
+    p = Problem(lib, torch, M, 520, 656, 16)
+    lib.theta_device_status()
+    lib.theta_selftest_wait_timeout(20)
+    p.call()
+    with pytest.raises(lib.ThetaError) as err:
+        lib.theta_device_status()
+    assert err.value.status == -5
+    p.call()
+    lib.theta_device_status()
+    p.check()
+
+
+def test_outputs_past_32_bit_offsets(lib, torch):
+    """Y, and the row encoder's input and codes, of more than 2^31 elements."""
+    M, O, I = 131072, 21504, 16
+    p = Problem(lib, torch, 8, O, I, 8)
+    X = p.Xd.repeat(M // 8, 1)
+    xc, xs = encode_rows(lib, torch, X)
+    Y = torch.empty(M, O, dtype=torch.bfloat16, device="cuda")
+    work = torch.empty(lib.theta_workspace_size(lib.THETA_OP_LINEAR_FORWARD_FP8, M, O, I, 8, lib.THETA_BF16),
+                       dtype=torch.uint8, device="cuda")
+    lib.theta_linear_forward_fp8(X, xc, xs, p.wc, p.ws, p.sd, p.Ud, p.Vd, Y, work)
+    lib.theta_device_status()
+    for at in (0, M // 2, M - 8):
+        p.check(Y=Y[at:at + 8], what=f"tokens from {at}")
+    del X, xc, xs, Y
+    M, I = 40000, 65536
+    X = torch.randn(8, I, device="cuda").bfloat16().repeat(M // 8, 1)
+    c, s = encode_rows(lib, torch, X)
+    lib.theta_device_status()
+    cr, sr = oracle.fp8_quantize_rows(host(X[:8]))
+    for at in (0, M - 8):
+        assert np.array_equal(c[at:at + 8].cpu().numpy(), cr) and np.array_equal(s[:, at:at + 8].cpu().numpy(), sr)
 
 
 def test_two_calls_at_once_on_two_streams(lib, torch):

@@ -144,6 +144,20 @@ def test_zero_heads_huge_heads_and_bad_values(lib, torch):
         check(ys[m, hh][None], xs[m, hh][None], 64, None, 0.0, 1e-6, pos[m:m + 1], f, False, "f32")
 
 
+def test_past_32_bit_offsets_in_place(lib, torch):
+    """A query buffer of more than 2^31 elements, in place, many rounds of tokens a block."""
+    M, heads, D = 300000, 30, 256
+    rng = np.random.default_rng(6)
+    x = draw(rng, 8, heads, D, "bf16")
+    X = dev(x, "bf16").repeat(M // 8, 1)
+    f = frequencies(D // 2)
+    pos = torch.arange(M, device="cuda")
+    lib.theta_qk_norm_rope(X, None, None, None, pos, torch.from_numpy(f).cuda(), X, None, D)
+    lib.theta_device_status()
+    for at in (0, M // 2, M - 8):
+        check(host(X[at:at + 8]), x, D, None, 0.0, 1e-6, np.arange(at, at + 8), f, False, "bf16", f"token {at}")
+
+
 def test_captured_other_stream_and_side_by_side(lib, torch):
     rng = np.random.default_rng(5)
     x = draw(rng, 40, 6, 128, "bf16")
