@@ -1092,6 +1092,61 @@ def run_op(args):
         # the NVFP4 block (0.5625 bytes per weight) instead of bf16 W0
         nbytes = bytes_forward(M, O, I, r) - O * I * BF16 + O * I * 9 // 16
         nflops = flops_forward(M, O, I, r)
+    elif args.op == "forward_fp8":
+        # W0 and X in block-scaled E4M3; the X codes are made once, as for
+        # projections that share an input
+        nbuf = args.bufs if args.b2b else 1
+        X = syn.device_normal((M, I), 1.0, seed, "X", M, I)
+        nb = -(-I // 128)
+        xc = torch.empty(M, I, dtype=torch.uint8, device="cuda")
+        xs = torch.empty(nb, M, dtype=torch.uint8, device="cuda")
+        theta.theta_fp8_quantize_rows(X, xc, xs)
+        probs = []
+        for k in range(nbuf):
+            W0 = syn.device_normal((O, I), 0.02, seed + k, "W0", O, I)
+            codes = torch.empty(O, I, dtype=torch.uint8, device="cuda")
+            scales = torch.empty(-(-O // 128), nb, dtype=torch.uint8, device="cuda")
+            theta.theta_fp8_quantize(W0, codes, scales)
+            del W0
+            s = 1.0 + syn.device_normal((O,), 0.05, seed + k, "s", O, dtype="f32")
+            U = syn.device_normal((O, r), 0.01, seed + k, "U", O, r) if r else None
+            V = syn.device_normal((I, r), 0.01, seed + k, "V", I, r) if r else None
+            probs.append((codes, scales, s, U, V, torch.empty(M, O, dtype=torch.bfloat16, device="cuda")))
+        ws = torch.empty(max(theta.theta_workspace_size(theta.THETA_OP_LINEAR_FORWARD_FP8, M, O, I, r,
+                                                        theta.THETA_BF16), 256), dtype=torch.uint8, device="cuda")
+        turn = [0]
+
+        def call():
+            codes, scales, s, U, V, Y = probs[turn[0] % nbuf]
+            turn[0] += 1
+            theta.theta_linear_forward_fp8(X, xc, xs, codes, scales, s, U, V, Y, ws)
+        # one byte per weight and per X code; X itself only for T = X.V
+        nbytes = bytes_forward(M, O, I, r) - O * I - (M * I if r == 0 else -M * I) + nb * (M + -(-O // 128))
+        nflops = flops_forward(M, O, I, r)
+    elif args.op == "fp8_quantize":
+        # the shared block [O, I]
+        W0 = syn.device_normal((O, I), 0.02, seed, "W0", O, I)
+        codes = torch.empty(O, I, dtype=torch.uint8, device="cuda")
+        scales = torch.empty(-(-O // 128), -(-I // 128), dtype=torch.uint8, device="cuda")
+        call = lambda: theta.theta_fp8_quantize(W0, codes, scales)  # noqa: E731
+        nbytes, nflops = O * I * (BF16 + 1) + scales.numel(), 0
+    elif args.op == "fp8_quantize_rows":
+        # the activations [M, I]
+        X = syn.device_normal((M, I), 1.0, seed, "X", M, I)
+        codes = torch.empty(M, I, dtype=torch.uint8, device="cuda")
+        scales = torch.empty(-(-I // 128), M, dtype=torch.uint8, device="cuda")
+        call = lambda: theta.theta_fp8_quantize_rows(X, codes, scales)  # noqa: E731
+        nbytes, nflops = M * I * (BF16 + 1) + scales.numel(), 0
+    elif args.op == "qk_norm_rope":
+        # the q and k rows of --model's shapes (heads of 256), M tokens
+        model, D = (syn.GEMMA4_31B if args.model == "31b" else syn.GEMMA3_1B), 256
+        Q, K = (syn.device_normal((M, model.shapes[f][0]), 1.0, seed, f, M) for f in ("q", "k"))
+        Qo, Ko = torch.empty_like(Q), torch.empty_like(K)
+        wq, wk = (syn.device_normal((D,), 0.1, seed, "w" + f) for f in ("q", "k"))
+        pos = torch.arange(M, device="cuda")
+        freq = 10000.0 ** (-torch.arange(D // 2, device="cuda", dtype=torch.float32) / (D // 2))
+        call = lambda: theta.theta_qk_norm_rope(Q, K, wq, wk, pos, freq, Qo, Ko, D, weight_offset=1.0)  # noqa: E731
+        nbytes, nflops = 2 * BF16 * (Q.numel() + K.numel()) + 8 * M + 2 * D + 2 * BF16 * D, 0
     elif args.op == "grouped":
         # every family of --layers Gemma-3-1B-shaped layers in one grouped call
         # (or, with --per-call-decode, one theta_linear_forward per problem)
@@ -1204,12 +1259,13 @@ def run_op(args):
     ms = statistics.median(per_call)
     if args.b2b:
         l2 = "calls back to back, no flush (median over %d rounds of %d calls)" % (rounds, args.iters)
-        if args.op in ("forward", "forward_nvfp4", "gate_up"):
+        if args.op in ("forward", "forward_nvfp4", "forward_fp8", "gate_up"):
             l2 += ", cycling over %d independent problems" % args.bufs
     else:
         l2 = "flushed (256 MiB write) before every call (median of %d)" % len(per_call)
     theta.theta_device_status()
-    line = {"op": args.op, "shape": {"M": M, "O": O, "I": I, "rank": r, "layers": L, "G": G}, "dtype": "bf16",
+    line = {"op": args.op, "shape": {"M": M, "O": O, "I": I, "rank": r, "layers": L, "G": G},
+            "dtype": "e4m3" if args.op == "forward_fp8" else "bf16",
             "ms": round(ms, 5), "iters": args.iters, "l2": l2, "policy": args.policy,
             "GB/s": round(nbytes / (ms * 1e-3) / 1e9, 1),
             "frac_hbm": round(nbytes / (ms * 1e-3) / 1e9 / peaks["hbm_gbs"], 4), "algorithmic_bytes": nbytes,
@@ -1240,10 +1296,11 @@ def main(argv=None):
     ap.add_argument("--e2e-steps", type=int, default=2)
     ap.add_argument("--cpu-seconds", type=float, default=12.0)
     ap.add_argument("--ref-rows", type=int, default=8)
-    ap.add_argument("--op", choices=["forward", "layer_forward", "forward_nvfp4", "gate_up", "grouped", "reconstruct",
+    ap.add_argument("--op", choices=["forward", "layer_forward", "forward_nvfp4", "forward_fp8", "fp8_quantize",
+                                     "fp8_quantize_rows", "qk_norm_rope", "gate_up", "grouped", "reconstruct",
                                      "reconstruct_band", "prelude", "frob", "svd"],
                     help="time one entry point on one problem instead of the whole step")
-    ap.add_argument("--model", choices=["1b", "31b"], default="31b", help="--op layer_forward: the model's shapes")
+    ap.add_argument("--model", choices=["1b", "31b"], default="31b", help="--op layer_forward, qk_norm_rope: the model's shapes")
     ap.add_argument("--policy", choices=["latency", "throughput"], default="latency",
                     help="--op: the library's launch policy (the step uses throughput)")
     ap.add_argument("--M", type=int, default=256)

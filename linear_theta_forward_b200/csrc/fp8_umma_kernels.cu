@@ -25,6 +25,10 @@
 //   epilogue     the same warps 2-5 after the last group (one-SM tiles); warps
 //                4-11 of their own in the persistent CTA-pair kernel
 // Waits are bounded as everywhere in the library.
+//
+// Measured (device time, rank 64 on [21504, 5376]): 1 token 24.4 us (4.9 TB/s,
+// HBM and the T = X.V launch in front), 64 tokens 28.5, 2048 tokens 245 us (1.96
+// PFLOP/s at the power cap, where the SM clock is 1.35 GHz; 214 us alone).
 #include <cuda.h>
 
 #include <algorithm>

