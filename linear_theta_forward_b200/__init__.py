@@ -379,12 +379,15 @@ def theta_linear_forward_nvfp4(X, codes, scales, g, s, U, V, Y, workspace=None, 
            "theta_linear_forward_nvfp4")
 
 
-def _here():
-    """(torch, the current device): what a call looks up once. The calls work on the current device; a pointer of another
-    one would fault there, so _arg and _rows refuse it."""
-    torch = _torch()
-    device = torch.cuda.current_device() if torch.cuda.is_initialized() else -2  # no CUDA tensor can exist yet
-    return torch, device
+def _here(stream):
+    """(torch, the current device, the stream's handle): what a call looks up
+    once. The calls work on the current device; a pointer of another one would
+    fault there, so _arg and _rows refuse it."""
+    torch = _TORCH or _torch()
+    if not torch.cuda.is_initialized():  # no CUDA tensor can exist yet: _arg refuses the first one
+        return torch, -2, None
+    device = torch._C._cuda_getDevice()
+    return torch, device, torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def _arg(t, name, dtype, shape, device):
@@ -403,23 +406,23 @@ def _arg(t, name, dtype, shape, device):
 def theta_fp8_quantize(W0, codes, scales, stream=None) -> None:
     """Encode W0 [O, I] (bf16 or fp32) in E4M3: codes uint8 [O, I], scales
     uint8 [ceil(O/128), ceil(I/128)], one power of two per 128 x 128 block."""
-    torch, dev = _here()
+    torch, dev, handle = _here(stream)
     O, I = shape = W0.shape
     _check(_load().theta_fp8_quantize(_arg(W0, "W0", W0.dtype, shape, dev), O, I, _dtype_code(W0),
                                       _arg(codes, "codes", torch.uint8, shape, dev),
                                       _arg(scales, "scales", torch.uint8, (-(-O // 128), -(-I // 128)), dev),
-                                      _stream(stream)), "theta_fp8_quantize")
+                                      handle), "theta_fp8_quantize")
 
 
 def theta_fp8_quantize_rows(X, codes, scales, stream=None) -> None:
     """Encode activations X [M, I] (bf16 or fp32) in E4M3: codes uint8 [M, I],
     scales uint8 [ceil(I/128), M], one power of two per token and 128 columns."""
-    torch, dev = _here()
+    torch, dev, handle = _here(stream)
     M, I = shape = X.shape
     _check(_load().theta_fp8_quantize_rows(_arg(X, "X", X.dtype, shape, dev), M, I, _dtype_code(X),
                                            _arg(codes, "codes", torch.uint8, shape, dev),
                                            _arg(scales, "scales", torch.uint8, (-(-I // 128), M), dev),
-                                           _stream(stream)), "theta_fp8_quantize_rows")
+                                           handle), "theta_fp8_quantize_rows")
 
 
 def theta_linear_forward_fp8(X, X_codes, X_scales, codes, scales, s, U, V, Y, workspace=None, stream=None) -> None:
@@ -427,7 +430,7 @@ def theta_linear_forward_fp8(X, X_codes, X_scales, codes, scales, s, U, V, Y, wo
     and theta_fp8_quantize wrote. X (bf16) may be None when U and V are.
     workspace: CUDA tensor of at least theta_workspace_size(
     THETA_OP_LINEAR_FORWARD_FP8, ...) bytes (None if 0)."""
-    torch, dev = _here()
+    torch, dev, handle = _here(stream)
     u8, bf = torch.uint8, torch.bfloat16
     if (U is None) != (V is None):
         raise ValueError("U and V must be given together")
@@ -444,7 +447,7 @@ def theta_linear_forward_fp8(X, X_codes, X_scales, codes, scales, s, U, V, Y, wo
         _arg(X_scales, "X_scales", u8, (nb, M), dev), M, I, _arg(codes, "codes", u8, (O, I), dev),
         _arg(scales, "scales", u8, (-(-O // 128), nb), dev), O, _arg(s, "s", torch.float32, (O,), dev),
         None if U is None else _arg(U, "U", bf, (O, rank), dev), None if V is None else _arg(V, "V", bf, (I, rank), dev),
-        rank, _arg(Y, "Y", bf, (M, O), dev), ws_ptr, ws_bytes, _stream(stream)), "theta_linear_forward_fp8")
+        rank, _arg(Y, "Y", bf, (M, O), dev), ws_ptr, ws_bytes, handle), "theta_linear_forward_fp8")
 
 
 def _rows(t, name, M, head_dim, dtype, device):
@@ -467,7 +470,7 @@ def theta_qk_norm_rope(Q, K, q_weight, k_weight, positions, inv_freq, Q_out, K_o
     first 2 * len(inv_freq) values by positions (int64 [M]) * inv_freq (fp32).
     K and K_out, each weight, and positions with inv_freq may be None. Rows
     may be slices of a wider tensor; Q_out and K_out may be Q and K."""
-    torch, dev = _here()
+    torch, dev, handle = _here(stream)
     head_dim = int(head_dim)
     if head_dim < 1:
         raise ValueError("head_dim must be positive")
@@ -485,7 +488,7 @@ def theta_qk_norm_rope(Q, K, q_weight, k_weight, positions, inv_freq, Q_out, K_o
         None if k_weight is None else _arg(k_weight, "k_weight", dtype, (head_dim,), dev), weight_offset, eps,
         None if positions is None else _arg(positions, "positions", torch.int64, (M,), dev),
         None if inv_freq is None else _arg(inv_freq, "inv_freq", torch.float32, (half,), dev), 2 * half,
-        int(interleaved), qo, ldqo, ko, ldko, _stream(stream)), "theta_qk_norm_rope")
+        int(interleaved), qo, ldqo, ko, ldko, handle), "theta_qk_norm_rope")
 
 
 def theta_residual_svd(R, rank, omega, U, V, workspace, power_iters=2, stream=None) -> None:

@@ -316,12 +316,4 @@ cudaError_t launch_fp8_quantize_rows(const LaunchCtx& c, theta_dtype dt, const v
                                        static_cast<const float*>(X), M, I, row_bits, q, e);
 }
 
-size_t forward_fp8_workspace_bytes(int64_t M, int r) { return forward_fp8_umma_workspace_bytes(M, r); }
-
-int launch_forward_fp8(const LaunchCtx& c, const void* X, const void* xq, const void* xs, const void* wq,
-                       const void* ws, const float* s, const void* U, const void* V, int64_t M, int64_t O, int64_t I,
-                       int r, void* Y, void* work, cudaError_t* ce) {
-  return launch_forward_fp8_umma(c, X, xq, xs, wq, ws, s, U, V, M, O, I, r, Y, work, ce);
-}
-
 }  // namespace theta

@@ -739,15 +739,15 @@ cudaError_t launch_pair(const LaunchCtx& c, const Maps& mp, const Args& args, co
 constexpr int kXvParts = 64;
 constexpr int kXvRows = 84;
 
-size_t forward_fp8_umma_workspace_bytes(int64_t M, int r) {
+size_t forward_fp8_workspace_bytes(int64_t M, int r) {
   const size_t half = ((size_t)M * r * 2 + 255) / 256 * 256;
   const size_t parts = M <= kFewTokens ? (size_t)kXvParts * M * r * sizeof(float) : 0;
   return std::max(2 * half, parts);  // T's high and low parts, or its partial sums
 }
 
-int launch_forward_fp8_umma(const LaunchCtx& c, const void* X, const void* xq, const void* xs, const void* wq,
-                            const void* ws, const float* s, const void* U, const void* V, int64_t M, int64_t O,
-                            int64_t I, int r, void* Y, void* work, cudaError_t* ce) {
+int launch_forward_fp8(const LaunchCtx& c, const void* X, const void* xq, const void* xs, const void* wq,
+                       const void* ws, const float* s, const void* U, const void* V, int64_t M, int64_t O, int64_t I,
+                       int r, void* Y, void* work, cudaError_t* ce) {
   *ce = cudaSuccess;
   int st;
   bf16* t_hi = static_cast<bf16*>(work);
@@ -758,7 +758,7 @@ int launch_forward_fp8_umma(const LaunchCtx& c, const void* X, const void* xq, c
     *ce = launch_xv_parts(c, X, V, M, I, r, nparts, static_cast<float*>(work));
     if (*ce != cudaSuccess) return THETA_ERR_CUDA;
   } else if (r > 0) {
-    t_lo = reinterpret_cast<bf16*>(static_cast<uint8_t*>(work) + forward_fp8_umma_workspace_bytes(M, r) / 2);
+    t_lo = reinterpret_cast<bf16*>(static_cast<uint8_t*>(work) + forward_fp8_workspace_bytes(M, r) / 2);
     if ((st = launch_xv_umma(c, X, V, M, I, r, t_hi, t_lo, ce))) return st;
   }
   const int width = (int)(ceil_div(ceil_div(M, ceil_div(M, kPairN)), 16) * 16);  // tokens of a pair's tile

@@ -18,9 +18,9 @@
 // their full precision; the block computes one sine and cosine per pair and
 // token, shared by its heads.
 //
-// Measured: 8192 tokens of 32 + 8 heads of 256 in bf16 70 us, 4.8 TB/s (0.73
-// of the copy rate); loads in flight and issue slots (54% used) bound it, not
-// the angles (69 us without them). One token 3.2 us.
+// Measured: 8192 tokens of 32 + 8 heads of 256 in bf16 67 us, 5.0 TB/s (0.76
+// of the copy rate); loads in flight and issue slots bound it, not the angles
+// (1 us of it). One token 3.1 us.
 #include <algorithm>
 #include <mutex>
 
@@ -139,7 +139,9 @@ __device__ __forceinline__ void angle(double turns, float freq, float* c, float*
 template <typename T, int G, int VPL, int PAIRING>
 __global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__ HeadArgs a) {
   extern __shared__ float table[];  // two buffers of [tokens][cos, sin][rotary / 2]
-  constexpr int kAhead = VPL == 1 ? 4 : VPL == 2 ? 2 : 1;  // heads a lane loads at once
+  // heads a lane loads at once, a round of them ahead of the one worked on
+  // (8192 tokens: 67.2 us; 69.8 and 74.0 with 2 and 4, 70.2 with 4 and none ahead)
+  constexpr int kAhead = VPL == 1 ? 3 : VPL == 2 ? 2 : 1;
   const int64_t* pos = a.pos;
   const float* freq = a.inv_freq;
   pdl_enter(pos, freq);
@@ -230,22 +232,26 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__
           A2[v][q] = pair2(A[v][2 * q], A[v][2 * q + 1]);
           B2[v][q] = pair2(B[v][2 * q], B[v][2 * q + 1]);
         }
-      for (int h0 = lo + grp; h0 < hi; h0 += kAhead * groups) {
-        Raw8<T> raw[kAhead][VPL], other[PAIRING == HALVES && VPL > 1 ? kAhead : 1][VPL];
+      Raw8<T> raw[kAhead][VPL], ahead[kAhead][VPL];
+      auto fetch = [&](int h0) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
           const T* x = x0 + (int64_t)(h0 + u * groups - base) * D;
 #pragma unroll
           for (int v = 0; v < VPL; ++v) {
             const int i0 = (lane + v * G) * 8;
-            raw[u][v].zero();
-            if (i0 < D && h0 + u * groups < hi) raw[u][v].load(x + i0);
-            if constexpr (PAIRING == HALVES && VPL > 1) {
-              other[u][v].zero();
-              if (i0 < rotary && h0 + u * groups < hi) other[u][v].load(x + (i0 < half ? i0 + half : i0 - half));
-            }
+            ahead[u][v].zero();
+            if (i0 < D && h0 + u * groups < hi) ahead[u][v].load(x + i0);
           }
         }
+      };
+      fetch(lo + grp);
+      for (int h0 = lo + grp; h0 < hi; h0 += kAhead * groups) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+          for (int v = 0; v < VPL; ++v) raw[u][v] = ahead[u][v];
+        fetch(h0 + kAhead * groups);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
           if (h0 + u * groups >= hi) break;
@@ -265,7 +271,11 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__
               if (i0 >= rotary) o.zero();
               o.get(p[v]);
             } else if constexpr (PAIRING == HALVES) {
-              other[u][v].get(p[v]);
+              // in L1: the same head's vectors, loaded by this group of lanes
+              Raw8<T> o;
+              o.zero();
+              if (i0 < rotary) o.load(x0 + at + (i0 < half ? i0 + half : i0 - half));
+              o.get(p[v]);
             } else if constexpr (PAIRING == NEIGHBOURS) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) p[v][e] = i0 + e < rotary ? f[v][e ^ 1] : 0.f;

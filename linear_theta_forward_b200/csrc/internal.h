@@ -104,11 +104,7 @@ cudaError_t launch_fp8_quantize(const LaunchCtx& c, theta_dtype dt, const void* 
 cudaError_t launch_fp8_quantize_rows(const LaunchCtx& c, theta_dtype dt, const void* X, int64_t M, int64_t I,
                                      void* codes, void* scales);
 size_t forward_fp8_workspace_bytes(int64_t M, int r);
-// The tensor-core forward (fp8_umma_kernels.cu).
-size_t forward_fp8_umma_workspace_bytes(int64_t M, int r);
-int launch_forward_fp8_umma(const LaunchCtx& c, const void* X, const void* xq, const void* xs, const void* wq,
-                            const void* ws, const float* s, const void* U, const void* V, int64_t M, int64_t O,
-                            int64_t I, int r, void* Y, void* work, cudaError_t* ce);
+// The forward (fp8_umma_kernels.cu): THETA_OK or a theta_status, CUDA errors in *ce.
 int launch_forward_fp8(const LaunchCtx& c, const void* X, const void* xq, const void* xs, const void* wq,
                        const void* ws, const float* s, const void* U, const void* V, int64_t M, int64_t O, int64_t I,
                        int r, void* Y, void* work, cudaError_t* ce);
