@@ -165,7 +165,8 @@ class Problem:
         assert (self.guard[:256] == 7).all() and (self.guard[256 + M * O:] == 7).all(), "wrote outside Y"
 
 
-SHAPES = [(1, 8, 16, 0), (1, 256, 1152, 32), (1, 1032, 640, 8), (2, 392, 336, 24), (2, 264, 400, 256), (1, 136, 16, 200), (3, 136, 144, 16), (1, 6912, 1152, 0),
+SHAPES = [(1, 8, 16, 0), (1, 256, 1152, 32), (1, 1032, 640, 8), (2, 392, 336, 24), (2, 264, 400, 256), (1, 136, 16, 200), (1, 264, 256, 256), (2, 264, 272, 240), (1, 520, 8192, 8),
+          (2, 520, 8208, 8), (2, 136, 1648, 40), (3, 136, 144, 16), (1, 6912, 1152, 0),
           (5, 128, 128, 8), (8, 264, 4096, 64), (15, 1024, 1152, 40), (16, 2048, 5376, 64), (17, 128, 2064, 0),
           (31, 520, 1296, 256), (33, 776, 272, 32), (64, 1152, 6912, 32), (65, 136, 512, 128), (100, 1000, 1168, 24),
           (128, 256, 1152, 0), (129, 384, 256, 8), (200, 2056, 1168, 24), (256, 1024, 1152, 64), (257, 264, 656, 16),
