@@ -55,6 +55,15 @@ int make_ctx(void* stream, LaunchCtx* ctx) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return fail_cuda(e, "cudaGetDevice");
   if (dev < 0 || dev >= kMaxDevices) return fail(THETA_ERR_UNSUPPORTED, "device ordinal %d", dev);
+  // A thread's first call may come before any runtime call has made the
+  // device's context current in it; encoding a TMA descriptor, a driver call,
+  // needs one.
+  thread_local int t_bound = -1;
+  if (t_bound != dev) {
+    e = cudaSetDevice(dev);
+    if (e != cudaSuccess) return fail_cuda(e, "cudaSetDevice");
+    t_bound = dev;
+  }
   {
     std::lock_guard<std::mutex> lk(g_mu);
     DeviceState& d = g_dev[dev];

@@ -344,6 +344,78 @@ def test_two_calls_at_once_on_two_streams(lib, torch):
         p.check()
 
 
+def test_first_calls_of_fresh_threads(lib, torch):
+    """Several host threads, each making its first CUDA call through the
+    library, on streams of their own: FP8 and bf16 forwards."""
+    import threading
+    ps = [Problem(lib, torch, M, 520, 656, 16, seed=M) for M in (1, 2, 40, 300, 40, 300)]
+    streams = [torch.cuda.Stream() for _ in ps]
+    X, W = torch.randn(40, 656, device="cuda").bfloat16(), torch.randn(520, 656, device="cuda").bfloat16()
+    s, Y = torch.ones(520, device="cuda"), torch.zeros(40, 520, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    failed = []
+
+    def guarded(call):
+        try:
+            for _ in range(10):
+                call()
+        except Exception as e:  # noqa: BLE001 - reported below
+            failed.append(e)
+    calls = [lambda p=p, st=st: p.call(stream=st.cuda_stream) for p, st in zip(ps, streams)]
+    side = torch.cuda.Stream()
+    calls.append(lambda: lib.theta_linear_forward(X, W, s, None, None, Y, None, stream=side.cuda_stream))
+    threads = [threading.Thread(target=guarded, args=(c,)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    lib.theta_device_status()
+    assert not failed, failed
+    for p in ps:
+        p.check()
+    ref = host(X) @ host(W).T
+    assert np.abs(host(Y) - ref).max() <= 2e-2 * np.sqrt(np.mean(ref ** 2))
+
+
+@pytest.mark.parametrize("what", ["blocks", "rows", "forward 1", "forward 4", "forward 300", "heads"])
+def test_first_call_of_a_process_captured(what):
+    """A process whose first call of the library is made inside a graph capture."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import sys, torch
+import linear_theta_forward_b200 as th
+op, M, bf = sys.argv[1], int(sys.argv[2]), torch.bfloat16
+r = lambda *s: torch.randn(*s, device="cuda").to(bf)
+z = lambda *s: torch.full(s, 127, dtype=torch.uint8, device="cuda")
+W, X, U, V, s, Q = r(256, 400), r(M, 400), r(256, 16), r(400, 16), torch.ones(256, device="cuda"), r(M, 256)
+wc, ws, xc, xs = z(256, 400) % 64, z(2, 4), z(M, 400) % 64, z(4, M)
+Y, Qo = torch.zeros(M, 256, dtype=bf, device="cuda"), torch.zeros_like(Q)
+work, pos, f = z(1 << 18), torch.arange(M, device="cuda"), torch.ones(32, device="cuda")
+call, out = {"blocks": (lambda: th.theta_fp8_quantize(W, wc, ws), wc),
+             "rows": (lambda: th.theta_fp8_quantize_rows(X, xc, xs), xc),
+             "forward": (lambda: th.theta_linear_forward_fp8(X, xc, xs, wc, ws, s, U, V, Y, work), Y),
+             "heads": (lambda: th.theta_qk_norm_rope(Q, None, None, None, pos, f, Qo, None, 64), Qo)}[op]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    call()
+g.replay()
+th.theta_device_status()
+a = out.clone()
+out.zero_()
+call()
+th.theta_device_status()
+assert torch.equal(a, out) and a.float().abs().sum() > 0
+"""
+    op, _, m = what.partition(" ")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", code, op, m or "4"], cwd=root, timeout=120, capture_output=True, text=True)
+    assert done.returncode == 0, done.stderr[-2000:]
+
+
 def test_attention_inputs_together(lib, torch):
     """One token batch quantized once, the q and k projections over it in FP8,
     the heads normed and rotated in place -- against the oracle's chain, each
