@@ -4,6 +4,8 @@
 // rejected call leaves device memory untouched. Kernels run on the caller's
 // stream; nothing here allocates device memory or synchronises (except
 // theta_device_status, whose job is to synchronise).
+#include <cuda.h>
+
 #include <algorithm>
 #include <cstdarg>
 #include <cstdio>
@@ -50,20 +52,41 @@ std::mutex g_mu;
 
 std::atomic<int> g_policy{THETA_POLICY_LATENCY};
 
+using CtxGetCurrentFn = CUresult (*)(CUcontext*);
+
+// A call works in the CUDA context that is current in its thread, as every
+// runtime call does, whichever context that is. A thread may have none: its
+// first CUDA call may be this one, or its context may have been taken off
+// since. Encoding a TMA descriptor, a driver call, needs one, so the device's
+// primary context is made current then, and only then: setting the device
+// while the caller's own context is current would replace it.
+int bind_context() {
+  static CtxGetCurrentFn get_current = nullptr;
+  static std::once_flag once;
+  static cudaError_t status = cudaSuccess;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    status = cudaGetDriverEntryPoint("cuCtxGetCurrent", &p, cudaEnableDefault, &q);
+    if (status == cudaSuccess && q != cudaDriverEntryPointSuccess) status = cudaErrorSymbolNotFound;
+    get_current = reinterpret_cast<CtxGetCurrentFn>(p);
+  });
+  if (status != cudaSuccess) return fail_cuda(status, "cuCtxGetCurrent");
+  CUcontext current = nullptr;
+  if (get_current(&current) == CUDA_SUCCESS && current) return THETA_OK;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaSetDevice(dev);
+  return e == cudaSuccess ? THETA_OK : fail_cuda(e, "cudaSetDevice");
+}
+
 int make_ctx(void* stream, LaunchCtx* ctx) {
+  int st = bind_context();
+  if (st) return st;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return fail_cuda(e, "cudaGetDevice");
   if (dev < 0 || dev >= kMaxDevices) return fail(THETA_ERR_UNSUPPORTED, "device ordinal %d", dev);
-  // A thread's first call may come before any runtime call has made the
-  // device's context current in it; encoding a TMA descriptor, a driver call,
-  // needs one.
-  thread_local int t_bound = -1;
-  if (t_bound != dev) {
-    e = cudaSetDevice(dev);
-    if (e != cudaSuccess) return fail_cuda(e, "cudaSetDevice");
-    t_bound = dev;
-  }
   {
     std::lock_guard<std::mutex> lk(g_mu);
     DeviceState& d = g_dev[dev];
