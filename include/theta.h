@@ -25,6 +25,11 @@
  *     host, enqueue kernels on `stream` (a cudaStream_t; NULL means the legacy
  *     default stream) and return. Errors found on the host are returned before
  *     anything is enqueued; nothing is written in that case.
+ *   - A call works in the CUDA context that is current in its thread and
+ *     leaves it current; where there is none it makes the device's primary
+ *     context current. Pointers and the stream belong to that context. At most
+ *     64 contexts of a process can call the library over its life
+ *     (THETA_ERR_UNSUPPORTED).
  *   - THETA_BF16 calls use the Tensor Memory Accelerator and need 16-byte
  *     aligned base pointers and row pitches that are multiples of 16 bytes
  *     (I, O and r multiples of 8); otherwise they return THETA_ERR_ALIGNMENT.
@@ -486,15 +491,15 @@ int theta_qk_norm_rope(const void* Q, int64_t ldq, int q_heads, const void* K, i
  *   - Capacity: the call needs theta_workspace_size(THETA_OP_LINEAR_FORWARD)
  *     bytes, at most 4 MiB (about M * rank <= 1,048,576). Larger requests
  *     return THETA_ERR_WORKSPACE before anything is enqueued.
- *   - Memory: every GPU that loads the library holds the 4 MiB array until
- *     the process exits. This entry point itself allocates nothing.
- *   - Sharing: all calls on a device use the same array. Calls ordered on one
+ *   - Memory: every CUDA context (usually one a GPU) that loads the library
+ *     holds the 4 MiB array as long as it lives. This entry point itself allocates nothing.
+ *   - Sharing: all calls in a context use the same array. Calls ordered on one
  *     stream are safe; calls whose kernels may overlap on the GPU (different
  *     streams without ordering between them) race on it and must not be made.
  *     Each call writes the scratch it reads, so leftovers from an earlier call
  *     do not matter.
- *   - Set-up: the first call on each device looks up the array's device
- *     address (cudaGetSymbolAddress, with that device current). Make that
+ *   - Set-up: the first call in each context looks up the array's device
+ *     address (cudaGetSymbolAddress). Make that
  *     first call before any stream capture begins.
  */
 int theta_linear_forward_noalloc(const void* X, int64_t M, int64_t I, const void* W0, int64_t O,

@@ -713,8 +713,8 @@ template <int BN, bool FEW = false>
 cudaError_t launch_tile(const LaunchCtx& c, const Maps& mp, Args args) {
   using C = Cfg<BN>;
   auto kern = fp8_tile_kernel<BN, FEW>;
-  static KernelInfo info[64];
-  cudaError_t e = prepare_kernel(&info[c.device], c.device, kern, kThreads, C::kSmemBytes, C::kTmemCols, true);
+  static KernelInfo info[kMaxContexts];
+  cudaError_t e = prepare_kernel(&info[c.slot], c.device, kern, kThreads, C::kSmemBytes, C::kTmemCols, true);
   if (e != cudaSuccess) return e;
   const int m_tiles = (int)ceil_div(args.rows, kBM), n_tiles = (int)ceil_div(args.cols, BN);
   args.splits = tile_splits(c, m_tiles, n_tiles, args.kb1);
@@ -723,9 +723,9 @@ cudaError_t launch_tile(const LaunchCtx& c, const Maps& mp, Args args) {
 }
 
 cudaError_t launch_pair(const LaunchCtx& c, const Maps& mp, const Args& args, const CUtensorMap& mY) {
-  static KernelInfo info[64];
+  static KernelInfo info[kMaxContexts];
   cudaError_t e =
-      prepare_kernel(&info[c.device], c.device, fp8_pair_kernel, kPairThreads, kPairSmemBytes, 512, false);
+      prepare_kernel(&info[c.slot], c.device, fp8_pair_kernel, kPairThreads, kPairSmemBytes, 512, false);
   if (e != cudaSuccess) return e;
   const int64_t tiles = ceil_div(args.rows, 2 * kBM) * ceil_div(args.cols, args.tile_tokens);
   const int64_t clusters = tiles < c.num_sms / 2 ? tiles : c.num_sms / 2;  // one CTA per SM

@@ -585,26 +585,26 @@ size_t fp4_smem_bytes(int64_t M, int64_t I) {
 // CTAs of this kernel one SM holds at once with `smem` bytes of dynamic
 // shared memory (registers, threads and shared memory decide).
 template <int M, bool FP4>
-int resident_ctas(int device, size_t smem) {
+int resident_ctas(int slot, size_t smem) {
   std::lock_guard<std::mutex> lk(setup_mutex());
-  static int cached[64] = {};
-  static size_t cached_smem[64] = {};
-  if (!cached[device] || cached_smem[device] != smem) {
+  static int cached[kMaxContexts] = {};
+  static size_t cached_smem[kMaxContexts] = {};
+  if (!cached[slot] || cached_smem[slot] != smem) {
     if (FP4) {
-      static bool opted[64] = {};
-      if (!opted[device]) {
+      static bool opted[kMaxContexts] = {};
+      if (!opted[slot]) {
         cudaFuncSetAttribute(gemv_rows_kernel<M, FP4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFp4SmemMax);
-        opted[device] = true;
+        opted[slot] = true;
       }
     }
     int n = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, gemv_rows_kernel<M, FP4>, kThreads, smem) != cudaSuccess ||
         n < 1)
       n = 1;
-    cached[device] = n;
-    cached_smem[device] = smem;
+    cached[slot] = n;
+    cached_smem[slot] = smem;
   }
-  return cached[device];
+  return cached[slot];
 }
 
 template <int M, bool FP4 = false>
@@ -616,7 +616,7 @@ cudaError_t launch_m(const LaunchCtx& c, GemvArgs a, const void* V) {
   }
   const size_t smem = FP4 ? fp4_smem_bytes(M, a.I) : 0;
   // the fewest rows per warp that keep every CTA resident in one wave
-  const int64_t capacity = (int64_t)c.num_sms * resident_ctas<M, FP4>(c.device, smem) * kWarps;
+  const int64_t capacity = (int64_t)c.num_sms * resident_ctas<M, FP4>(c.slot, smem) * kWarps;
   a.rpw = (int)ceil_div(a.O, capacity);
   // NVFP4 splits the rows evenly over one full wave; bf16 gives every warp rpw
   const int64_t grid = FP4 ? std::min(capacity / kWarps, ceil_div(a.O, (int64_t)kWarps))
@@ -674,11 +674,11 @@ bool launch_forward_grouped(const LaunchCtx& c, const theta_forward_problem* hos
     if (*e != cudaSuccess) return true;
   }
   auto go = [&](auto kern) {
-    static int cached[2][64] = {};
+    static int cached[2][kMaxContexts] = {};
     int n = 0;
     {
       std::lock_guard<std::mutex> lk(setup_mutex());
-      int& slot = cached[M - 1][c.device];
+      int& slot = cached[M - 1][c.slot];
       if (!slot && (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&slot, kern, kThreads, 0) != cudaSuccess ||
                     slot < 1))
         slot = 1;

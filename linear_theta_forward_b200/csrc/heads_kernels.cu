@@ -323,11 +323,11 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__
 template <typename T, int G, int VPL, int PAIRING>
 cudaError_t launch_heads(const LaunchCtx& c, HeadArgs a) {
   auto kern = heads_kernel<T, G, VPL, PAIRING>;
-  static int resident[64] = {};
+  static int resident[kMaxContexts] = {};
   int per_sm;
   {
     std::lock_guard<std::mutex> lk(setup_mutex());
-    int& slot = resident[c.device];
+    int& slot = resident[c.slot];
     if (!slot && (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&slot, kern, kThreads, 4 * kMaxDim) != cudaSuccess ||
                   slot < 1))
       slot = 1;

@@ -14,13 +14,24 @@ namespace theta {
 
 struct LaunchCtx {
   cudaStream_t stream;
-  unsigned* err;  // device error words of the current device
+  unsigned* err;  // device error words of the current context
   int num_sms;
   int device;
+  int slot;    // of the current context, below kMaxContexts
   int policy;  // theta_policy at the time of the call
 };
 
-// Held while a kernel's one-time, per-device set-up (attributes, occupancy
+// What is set up once -- a kernel's attributes and residency, the addresses
+// of the library's own device arrays -- belongs to a CUDA context, not to its
+// device (a second context of the device, or the primary one after a reset,
+// has its own), so it is remembered by the context's slot.
+constexpr int kMaxContexts = 64;
+
+// The context that a call works in: its slot, device and error words
+// (theta_api.cu). THETA_OK or a status whose message is set.
+int make_ctx(void* stream, LaunchCtx* ctx);
+
+// Held while a kernel's one-time, per-context set-up (attributes, occupancy
 // and cluster queries, the caches that remember them) runs, so that threads
 // making their first calls at once neither race on a cache nor read one that
 // is half written.

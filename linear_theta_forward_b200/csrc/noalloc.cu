@@ -10,9 +10,9 @@
 // output pointers. This entry point serves them from a fixed array compiled
 // into the library.
 //
-// The array below is ordinary device memory of the module: every GPU that
-// loads the library holds it, kScratchBytes of it, until the process exits.
-// All calls on a device share it, so two calls whose kernels overlap on the
+// The array below is ordinary device memory of the module: every CUDA context
+// that loads the library holds it, kScratchBytes of it, as long as it lives.
+// All calls in a context share it, so two calls whose kernels overlap on the
 // GPU (different streams, no ordering) race on it; calls ordered on one
 // stream are fine. Each call writes the part of the array it reads before it
 // reads it, so nothing has to start at zero and the previous call's contents
@@ -21,6 +21,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "internal.h"
 
 #define THETA_API extern "C" __attribute__((visibility("default")))
 
@@ -34,8 +35,7 @@ constexpr size_t kScratchBytes = size_t(4) << 20;  // 4 MiB: M * rank <= 1,048,5
 
 static __device__ __align__(256) unsigned char g_forward_scratch[kScratchBytes];
 
-constexpr int kMaxDevices = 64;
-void* g_scratch_ptr[kMaxDevices] = {};
+void* g_scratch_ptr[theta::kMaxContexts] = {};
 std::mutex g_scratch_mu;
 
 }  // namespace
@@ -63,26 +63,22 @@ THETA_API int theta_linear_forward_noalloc(const void* X, int64_t M, int64_t I, 
   }
   void* scratch = nullptr;
   if (need > 0) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
-      snprintf(msg, sizeof msg, "theta_linear_forward_noalloc: cudaGetDevice: %s", cudaGetErrorString(e));
-      return theta::report_error(THETA_ERR_CUDA, msg);
-    }
+    theta::LaunchCtx c;
+    if ((st = theta::make_ctx(stream, &c))) return st;
     std::lock_guard<std::mutex> lk(g_scratch_mu);
-    if (!g_scratch_ptr[dev]) {
-      // one-time set-up on this device: the host-side name of the array is a
+    if (!g_scratch_ptr[c.slot]) {
+      // one-time set-up in this context: the host-side name of the array is a
       // stand-in, so ask the runtime for the array's device address
       void* p = nullptr;
-      e = cudaGetSymbolAddress(&p, g_forward_scratch);
+      cudaError_t e = cudaGetSymbolAddress(&p, g_forward_scratch);
       if (e != cudaSuccess || p == nullptr) {
         snprintf(msg, sizeof msg, "theta_linear_forward_noalloc: cudaGetSymbolAddress: %s",
                  cudaGetErrorString(e));
         return theta::report_error(THETA_ERR_CUDA, msg);
       }
-      g_scratch_ptr[dev] = p;
+      g_scratch_ptr[c.slot] = p;
     }
-    scratch = g_scratch_ptr[dev];
+    scratch = g_scratch_ptr[c.slot];
   }
   return theta_linear_forward(X, M, I, W0, O, s, U, V, rank, dt, Y, scratch, kScratchBytes, stream);
 }

@@ -517,13 +517,13 @@ bool geometry(int64_t nv, int64_t per_row_bytes, int64_t item_cap, int* tpr, int
 template <typename T, bool BAND, int TPR, int VPT>
 cudaError_t launch_one(const LaunchCtx& c, const PreludeArgs& a, int grid, size_t smem) {
   auto kern = prelude_pipe_kernel<T, BAND, TPR, VPT>;
-  static bool opted[64] = {};
+  static bool opted[kMaxContexts] = {};
   std::unique_lock<std::mutex> lk(setup_mutex());
-  if (!opted[c.device]) {
+  if (!opted[c.slot]) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kSmemBudget + 128 + 2 * kMaxSlots * 8);
     if (e != cudaSuccess) return e;
-    opted[c.device] = true;
+    opted[c.slot] = true;
   }
   lk.unlock();
   return launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), smem, c.stream, 1, a);
@@ -642,18 +642,18 @@ bool geometry2(int64_t nv, int64_t row_bytes, int* tpr, int* vpt) {
 template <typename T, int TPR, int VPT, int LPI>
 cudaError_t launch_two(const LaunchCtx& c, const PreludeArgs& a, int grid, size_t smem) {
   auto kern = prelude_band2_kernel<T, TPR, VPT, LPI>;
-  static int resident[64] = {};  // CTAs per SM (registers and shared memory decide)
+  static int resident[kMaxContexts] = {};  // CTAs per SM (registers and shared memory decide)
   std::unique_lock<std::mutex> lk(setup_mutex());
-  if (!resident[c.device]) {
+  if (!resident[c.slot]) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kSmemBudget + 128 + 2 * kMaxSlots * 8);
     if (e != cudaSuccess) return e;
     int n = 0;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, kSmemBudget + 128 + 2 * kMaxSlots * 8);
     if (e != cudaSuccess) return e;
-    resident[c.device] = n < 1 ? 1 : n;
+    resident[c.slot] = n < 1 ? 1 : n;
   }
-  const int per_sm = resident[c.device];
+  const int per_sm = resident[c.slot];
   lk.unlock();
   // one wave: a CTA that waited for a slot of the SM would start its units late
   if (grid > c.num_sms * per_sm) grid = c.num_sms * per_sm;

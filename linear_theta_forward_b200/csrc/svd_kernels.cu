@@ -491,16 +491,16 @@ cudaError_t gemm(const LaunchCtx& c, const TA* A, const TB* B, int64_t M, int64_
                     M * N, out);
 }
 
-cudaError_t small_kernels_ready(int device) {
+cudaError_t small_kernels_ready(int slot) {
   std::lock_guard<std::mutex> lk(setup_mutex());
-  static bool done[64] = {};
-  if (done[device]) return cudaSuccess;
+  static bool done[kMaxContexts] = {};
+  if (done[slot]) return cudaSuccess;
   cudaError_t e = cudaFuncSetAttribute(chol_inv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)small_smem(kMaxSamples));
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(jacobi_eig_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)small_smem(kMaxSamples));
-  if (e == cudaSuccess) done[device] = true;
+  if (e == cudaSuccess) done[slot] = true;
   return e;
 }
 
@@ -549,7 +549,7 @@ template <typename T>
 cudaError_t run_svd(const LaunchCtx& c, const T* R, int64_t O, int64_t I, int r, int k, int power_iters,
                     const float* omega, T* U, T* V, float* ws) {
   const SvdPlan p = plan_svd(O, I, k, r);
-  cudaError_t e = small_kernels_ready(c.device);
+  cudaError_t e = small_kernels_ready(c.slot);
   if (e != cudaSuccess) return e;
   float* part = ws + p.part;
   float *Y = ws + p.y0, *Ytmp = ws + p.y1, *Zt = ws + p.z0, *Ztmp = ws + p.z1, *Bm = ws + p.bm;

@@ -41,68 +41,62 @@ int fail_cuda(cudaError_t e, const char* where) {
   return fail(THETA_ERR_CUDA, "%s: %s (%s)", where, cudaGetErrorString(e), cudaGetErrorName(e));
 }
 
-constexpr int kMaxDevices = 64;
-struct DeviceState {
-  bool ready = false;
+struct ContextState {
+  unsigned long long id = 0;
+  int device = 0;
   int num_sms = 0;
   unsigned* err = nullptr;
 };
-DeviceState g_dev[kMaxDevices];
+ContextState g_context[kMaxContexts];
+int g_contexts = 0;
 std::mutex g_mu;
 
 std::atomic<int> g_policy{THETA_POLICY_LATENCY};
 
-using CtxGetCurrentFn = CUresult (*)(CUcontext*);
-
-// A call works in the CUDA context that is current in its thread, as every
-// runtime call does, whichever context that is. A thread may have none: its
-// first CUDA call may be this one, or its context may have been taken off
-// since. Encoding a TMA descriptor, a driver call, needs one, so the device's
-// primary context is made current then, and only then: setting the device
-// while the caller's own context is current would replace it.
-int bind_context() {
-  static CtxGetCurrentFn get_current = nullptr;
+// The driver's names for the current context, looked up once.
+struct ContextFns {
+  CUresult (*get_current)(CUcontext*) = nullptr;
+  CUresult (*get_id)(CUcontext, unsigned long long*) = nullptr;
+  cudaError_t status = cudaSuccess;
+};
+const ContextFns& context_fns() {
+  static ContextFns f;
   static std::once_flag once;
-  static cudaError_t status = cudaSuccess;
   std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    status = cudaGetDriverEntryPoint("cuCtxGetCurrent", &p, cudaEnableDefault, &q);
-    if (status == cudaSuccess && q != cudaDriverEntryPointSuccess) status = cudaErrorSymbolNotFound;
-    get_current = reinterpret_cast<CtxGetCurrentFn>(p);
+    auto find = [](const char* name) -> void* {
+      void* p = nullptr;
+      cudaDriverEntryPointQueryResult q;
+      cudaError_t e = cudaGetDriverEntryPoint(name, &p, cudaEnableDefault, &q);
+      if (e == cudaSuccess && q != cudaDriverEntryPointSuccess) e = cudaErrorSymbolNotFound;
+      if (e != cudaSuccess) f.status = e;
+      return p;
+    };
+    f.get_current = reinterpret_cast<decltype(f.get_current)>(find("cuCtxGetCurrent"));
+    f.get_id = reinterpret_cast<decltype(f.get_id)>(find("cuCtxGetId"));
   });
-  if (status != cudaSuccess) return fail_cuda(status, "cuCtxGetCurrent");
-  CUcontext current = nullptr;
-  if (get_current(&current) == CUDA_SUCCESS && current) return THETA_OK;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaSetDevice(dev);
-  return e == cudaSuccess ? THETA_OK : fail_cuda(e, "cudaSetDevice");
+  return f;
 }
 
-int make_ctx(void* stream, LaunchCtx* ctx) {
-  int st = bind_context();
-  if (st) return st;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return fail_cuda(e, "cudaGetDevice");
-  if (dev < 0 || dev >= kMaxDevices) return fail(THETA_ERR_UNSUPPORTED, "device ordinal %d", dev);
-  {
-    std::lock_guard<std::mutex> lk(g_mu);
-    DeviceState& d = g_dev[dev];
-    if (!d.ready) {
-      e = cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev);
-      if (e != cudaSuccess) return fail_cuda(e, "cudaDeviceGetAttribute");
-      e = cudaGetSymbolAddress(reinterpret_cast<void**>(&d.err), g_err_words);
-      if (e != cudaSuccess) return fail_cuda(e, "cudaGetSymbolAddress(error words)");
-      d.ready = true;
-    }
-    ctx->num_sms = d.num_sms;
-    ctx->err = d.err;
+// The id, which no other context of the process ever has, of the context that
+// a call works in: the one current in its thread, as for every runtime call,
+// whichever context that is. A thread may have none: its first CUDA call may
+// be this one, or its context may have been taken off since. Encoding a TMA
+// descriptor, a driver call, needs one, so the device's primary context is
+// made current then, and only then: setting the device while the caller's own
+// context is current would replace it.
+int current_context(unsigned long long* id) {
+  const ContextFns& f = context_fns();
+  if (f.status != cudaSuccess) return fail_cuda(f.status, "cuCtxGetCurrent");
+  CUcontext current = nullptr;
+  if (f.get_current(&current) != CUDA_SUCCESS || !current) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaSetDevice(dev);
+    if (e != cudaSuccess) return fail_cuda(e, "cudaSetDevice");
+    if (f.get_current(&current) != CUDA_SUCCESS || !current)
+      return fail(THETA_ERR_CUDA, "no CUDA context is current after cudaSetDevice");
   }
-  ctx->device = dev;
-  ctx->stream = static_cast<cudaStream_t>(stream);
-  ctx->policy = g_policy.load(std::memory_order_relaxed);
+  if (f.get_id(current, id) != CUDA_SUCCESS) return fail(THETA_ERR_CUDA, "cuCtxGetId");
   return THETA_OK;
 }
 
@@ -124,6 +118,39 @@ size_t forward_ws_bytes(int64_t M, int r, theta_dtype dt) {
   } while (0)
 
 }  // namespace
+
+int make_ctx(void* stream, LaunchCtx* ctx) {
+  unsigned long long id = 0;
+  int st = current_context(&id);
+  if (st) return st;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    int slot = 0;
+    while (slot < g_contexts && g_context[slot].id != id) ++slot;
+    if (slot == kMaxContexts)
+      return fail(THETA_ERR_UNSUPPORTED, "more than %d CUDA contexts have called the library", kMaxContexts);
+    ContextState& s = g_context[slot];
+    if (slot == g_contexts) {
+      ContextState n;
+      n.id = id;
+      cudaError_t e = cudaGetDevice(&n.device);
+      if (e != cudaSuccess) return fail_cuda(e, "cudaGetDevice");
+      e = cudaDeviceGetAttribute(&n.num_sms, cudaDevAttrMultiProcessorCount, n.device);
+      if (e != cudaSuccess) return fail_cuda(e, "cudaDeviceGetAttribute");
+      e = cudaGetSymbolAddress(reinterpret_cast<void**>(&n.err), g_err_words);
+      if (e != cudaSuccess) return fail_cuda(e, "cudaGetSymbolAddress(error words)");
+      s = n;
+      ++g_contexts;
+    }
+    ctx->slot = slot;
+    ctx->device = s.device;
+    ctx->num_sms = s.num_sms;
+    ctx->err = s.err;
+  }
+  ctx->stream = static_cast<cudaStream_t>(stream);
+  ctx->policy = g_policy.load(std::memory_order_relaxed);
+  return THETA_OK;
+}
 
 std::mutex& setup_mutex() {
   static std::mutex mu;

@@ -1,5 +1,5 @@
 // Host side of the tensor-core launches: TMA descriptors and the one-time,
-// per-device kernel set-up.
+// per-context kernel set-up.
 #pragma once
 
 #include <cuda.h>
@@ -51,7 +51,7 @@ inline int make_map_box(CUtensorMap* m, const void* base, int64_t rows, int64_t 
   return THETA_OK;
 }
 
-// Per-device, per-kernel launch configuration: dynamic shared memory opt-in,
+// Per-context, per-kernel launch configuration: dynamic shared memory opt-in,
 // non-portable cluster sizes, and the number of co-resident CTAs per SM,
 // checked against tensor-memory capacity (co-resident CTAs must never need
 // more columns than an SM has, or allocation would stall).

@@ -1291,44 +1291,44 @@ template <int BN, int MODE>
 cudaError_t launch_tile_kernel(const LaunchCtx& c, const Maps& mp, Args args, int m_tiles, int n_tiles) {
   using C = Cfg<BN, MODE>;
   auto kern = umma_kernel<BN, MODE>;
-  static KernelInfo info[64];
-  cudaError_t e = prepare_kernel(&info[c.device], c.device, kern, kThreads, C::kSmemBytes, C::kTmemCols, true);
+  static KernelInfo info[kMaxContexts];
+  cudaError_t e = prepare_kernel(&info[c.slot], c.device, kern, kThreads, C::kSmemBytes, C::kTmemCols, true);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)m_tiles * n_tiles;
   // Tiles of 64 or more columns keep the tensor pipe busy: a second CTA on
   // the same SM adds no throughput, only split-K reduction work, so they
   // count one CTA per SM. Narrow (decode) tiles are bound by memory latency
   // and count every co-resident CTA.
-  const int capacity = c.num_sms * (BN >= 64 ? 1 : info[c.device].blocks_per_sm);
+  const int capacity = c.num_sms * (BN >= 64 ? 1 : info[c.slot].blocks_per_sm);
   // The throughput policy gives every CTA of the main projection a whole
   // tile. T = X.V keeps its split under both policies: it has one tile per
   // 128 tokens, so unsplit it is a single CTA walking all of K, a serial
   // latency chain that the forward behind it waits for.
   args.splits = (c.policy == THETA_POLICY_THROUGHPUT && MODE != MODE_XV)
                     ? 1
-                    : pick_splits(tiles, args.kb1, capacity, info[c.device].max_cluster);
+                    : pick_splits(tiles, args.kb1, capacity, info[c.slot].max_cluster);
   return launch_pdl(kern, dim3((unsigned)(n_tiles * args.splits), (unsigned)m_tiles, 1), dim3(kThreads), C::kSmemBytes,
                     c.stream, args.splits, mp.a1, mp.b1, mp.a2, mp.b2, mp.b3, mp.a1u, mp.a2u, mp.b2u, mp.b3u, args);
 }
 
 // The persistent CTA-pair kernel: one cluster of two per pair of SMs that
-// can hold one (the occupancy query, once per device), at most one per tile.
+// can hold one (the occupancy query, once per context), at most one per tile.
 // Y [M, O] is written by TMA in boxes of 128 rows of W0 (columns of Y) x one
 // tile's tokens.
 template <int MODE>
 cudaError_t launch_pair(const LaunchCtx& c, const Maps& mp, const Args& args, void* Y, cudaError_t* ce_map) {
   using C = PairCfg<MODE>;
   auto kern = pair_kernel<MODE>;
-  static KernelInfo info[64];
-  static int max_clusters[64];
+  static KernelInfo info[kMaxContexts];
+  static int max_clusters[kMaxContexts];
   CUtensorMap mY;
   if (make_map_box(&mY, Y, args.cols, args.rows, C::kN, kBM, CU_TENSOR_MAP_SWIZZLE_NONE, ce_map))
     return *ce_map;
-  cudaError_t e = prepare_kernel(&info[c.device], c.device, kern, C::kThreads, C::kSmemBytes, C::kTmemCols, false);
+  cudaError_t e = prepare_kernel(&info[c.slot], c.device, kern, C::kThreads, C::kSmemBytes, C::kTmemCols, false);
   if (e != cudaSuccess) return e;
   {
     std::lock_guard<std::mutex> lk(setup_mutex());
-    if (max_clusters[c.device] == 0) {
+    if (max_clusters[c.slot] == 0) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(2, 1, 1);
       cfg.blockDim = dim3(C::kThreads, 1, 1);
@@ -1346,11 +1346,11 @@ cudaError_t launch_pair(const LaunchCtx& c, const Maps& mp, const Args& args, vo
         if (!pending) cudaGetLastError();  // a refused query is not an error of this call
         n = c.num_sms / 2;                 // one CTA per SM
       }
-      max_clusters[c.device] = n;
+      max_clusters[c.slot] = n;
     }
   }
   const int64_t tiles = ceil_div(args.rows, 2 * kBM) * ceil_div(args.cols, C::kN);
-  const int64_t clusters = tiles < max_clusters[c.device] ? tiles : max_clusters[c.device];
+  const int64_t clusters = tiles < max_clusters[c.slot] ? tiles : max_clusters[c.slot];
   return launch_pdl(kern, dim3((unsigned)(2 * clusters), 1, 1), dim3(C::kThreads), C::kSmemBytes, c.stream, 2, mp.a1,
                     mp.b1, mp.a2, mp.b2, mp.b3, mp.a1u, mp.a2u, mp.b2u, mp.b3u, mY, args);
 }
@@ -1360,8 +1360,8 @@ cudaError_t launch_recon(const LaunchCtx& c, const CUtensorMap& mU, const CUtens
                          const CUtensorMap& mOut, const float* s, int O, int I) {
   using C = RecCfg<KB>;
   auto kern = recon_kernel<KB>;
-  static KernelInfo info[64];
-  cudaError_t e = prepare_kernel(&info[c.device], c.device, kern, kRecThreads, C::kSmemBytes, kRecN, false);
+  static KernelInfo info[kMaxContexts];
+  cudaError_t e = prepare_kernel(&info[c.slot], c.device, kern, kRecThreads, C::kSmemBytes, kRecN, false);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3((unsigned)ceil_div(I, kRecN), (unsigned)ceil_div(O, kBM), 1), dim3(kRecThreads),
                     C::kSmemBytes, c.stream, 1, mU, mV, mW0, mOut, s, O, I, c.err);
@@ -1371,8 +1371,8 @@ template <int KB>
 cudaError_t launch_band(const LaunchCtx& c, const CUtensorMap& mW0, const BandArgs& a) {
   using C = BandCfg<KB>;
   auto kern = recon_band_kernel<KB>;
-  static KernelInfo info[64];
-  cudaError_t e = prepare_kernel(&info[c.device], c.device, kern, kBandThreads, C::kSmemBytes, 2 * kRecN, false);
+  static KernelInfo info[kMaxContexts];
+  cudaError_t e = prepare_kernel(&info[c.slot], c.device, kern, kBandThreads, C::kSmemBytes, 2 * kRecN, false);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3((unsigned)ceil_div(a.I, kRecN), (unsigned)ceil_div(a.O, kBM), 1), dim3(kBandThreads),
                     C::kSmemBytes, c.stream, 1, mW0, a);
@@ -1677,8 +1677,8 @@ cudaError_t launch_svd_mma_t(const LaunchCtx& c, const CUtensorMap* maps, const 
                              int n_tiles) {
   using C = SvdCfg<R_LEFT>;
   auto kern = svd_mma_kernel<R_LEFT>;
-  static KernelInfo info[64];
-  cudaError_t e = prepare_kernel(&info[c.device], c.device, kern, kThreads, C::kSmemBytes, C::kTmemCols, false);
+  static KernelInfo info[kMaxContexts];
+  cudaError_t e = prepare_kernel(&info[c.slot], c.device, kern, kThreads, C::kSmemBytes, C::kTmemCols, false);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3((unsigned)n_tiles, (unsigned)m_tiles, (unsigned)a.splits), dim3(kThreads),
                     C::kSmemBytes, c.stream, 1, maps[0], maps[1], maps[2], maps[3], a);

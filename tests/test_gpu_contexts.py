@@ -125,6 +125,36 @@ for _ in range(2):  # descriptors to encode, on a thread that has bound the cont
 ok(cu.cuCtxSetCurrent(p))
 case.run()
 """,
+    "calls in turn in several contexts of one device": """
+contexts = [primary(), create(), create()]
+cases = []
+for n, c in enumerate(contexts):
+    ok(cu.cuCtxSetCurrent(c))
+    cases.append(Case(3 + n))
+for _ in range(2):
+    for c, case in zip(contexts, cases):
+        ok(cu.cuCtxSetCurrent(c))
+        case.run()
+        assert current() == c.value
+ok(cu.cuCtxDestroy_v2(contexts.pop()))
+last = create()  # where the destroyed one may have been
+Case(9).run()
+ok(cu.cuCtxSetCurrent(contexts[0]))
+cases[0].run()
+""",
+    "a timeout is reported in its own context": """
+contexts = [primary(), create()]
+cases = []
+for n, c in enumerate(contexts):
+    ok(cu.cuCtxSetCurrent(c))
+    cases.append(Case(20 + n))
+    cases[n].run()
+assert raw.theta_selftest_wait_timeout(20, cases[1].stream) == 0
+assert raw.theta_device_status(cases[1].stream) == -5
+for c, case in zip(contexts, cases):
+    ok(cu.cuCtxSetCurrent(c))
+    case.run()
+""",
 }
 
 
