@@ -435,7 +435,8 @@ int theta_fp8_quantize_rows(const void* X, int64_t M, int64_t I, theta_dtype dt,
  *   THETA_ERR_ALIGNMENT). M, O, I < 2^30, M and O at most 4,194,240 (else
  *   THETA_ERR_UNSUPPORTED).
  *   workspace: theta_workspace_size(THETA_OP_LINEAR_FORWARD_FP8, M, O, I,
- *   rank, THETA_BF16) bytes (holds T = X . V; 0 at rank 0).
+ *   rank, THETA_BF16) bytes (holds T = X . V; 0 at rank 0). The size does not
+ *   fall as M or rank grows: a buffer for the largest batch serves all.
  */
 int theta_linear_forward_fp8(const void* X, const void* X_codes, const void* X_scales, int64_t M, int64_t I,
                              const void* codes, const void* scales, int64_t O, const float* s, const void* U,

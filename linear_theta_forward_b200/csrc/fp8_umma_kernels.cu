@@ -739,10 +739,15 @@ cudaError_t launch_pair(const LaunchCtx& c, const Maps& mp, const Args& args, co
 constexpr int kXvParts = 64;
 constexpr int kXvRows = 84;
 
+// Bytes of one part of T, the offset of the low one.
+static size_t t_part_bytes(int64_t M, int r) { return ((size_t)M * r * 2 + 255) / 256 * 256; }
+
+// T's high and low parts, or its partial sums, whichever the call takes. The
+// partial sums of one or two tokens are larger than the parts of a few more,
+// so every size covers them: a buffer sized for a batch serves smaller ones.
 size_t forward_fp8_workspace_bytes(int64_t M, int r) {
-  const size_t half = ((size_t)M * r * 2 + 255) / 256 * 256;
-  const size_t parts = M <= kFewTokens ? (size_t)kXvParts * M * r * sizeof(float) : 0;
-  return std::max(2 * half, parts);  // T's high and low parts, or its partial sums
+  const size_t sums = (size_t)kXvParts * std::min<int64_t>(M, kFewTokens) * r * sizeof(float);
+  return std::max(2 * t_part_bytes(M, r), sums);
 }
 
 int launch_forward_fp8(const LaunchCtx& c, const void* X, const void* xq, const void* xs, const void* wq,
@@ -758,7 +763,7 @@ int launch_forward_fp8(const LaunchCtx& c, const void* X, const void* xq, const 
     *ce = launch_xv_parts(c, X, V, M, I, r, nparts, static_cast<float*>(work));
     if (*ce != cudaSuccess) return THETA_ERR_CUDA;
   } else if (r > 0) {
-    t_lo = reinterpret_cast<bf16*>(static_cast<uint8_t*>(work) + forward_fp8_workspace_bytes(M, r) / 2);
+    t_lo = reinterpret_cast<bf16*>(static_cast<uint8_t*>(work) + t_part_bytes(M, r));
     if ((st = launch_xv_umma(c, X, V, M, I, r, t_hi, t_lo, ce))) return st;
   }
   const int width = (int)(ceil_div(ceil_div(M, ceil_div(M, kPairN)), 16) * 16);  // tokens of a pair's tile

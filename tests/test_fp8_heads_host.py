@@ -105,6 +105,15 @@ def test_forward_refusals(lib):
             lib.theta_workspace_size(lib.THETA_OP_LINEAR_FORWARD_FP8, M, 8, 64, r, lib.THETA_BF16)
 
 
+def test_forward_workspace_does_not_fall_as_tokens_or_rank_grow(lib):
+    """One buffer, sized for the largest batch, serves every smaller one."""
+    counts = [*range(1, 70), 127, 128, 129, 240, 241, 2048, 100000]
+    table = [[lib.theta_workspace_size(lib.THETA_OP_LINEAR_FORWARD_FP8, M, 8, 64, r, lib.THETA_BF16)
+              for r in (0, 8, 24, 32, 64, 200, 256)] for M in counts]
+    assert all(a <= b for small, large in zip(table, table[1:]) for a, b in zip(small, large))
+    assert all(a <= b for sizes in table for a, b in zip(sizes, sizes[1:]))
+
+
 def test_heads_refusals(lib):
     raw = lib.lib
 

@@ -308,6 +308,22 @@ def test_work_after_a_timeout_is_flagged_then_recovers(lib, torch, M):
     p.check()
 
 
+@pytest.mark.parametrize("sized_for", [2, 3, 16, 64, 300])
+def test_one_workspace_for_a_batch_that_shrinks(lib, torch, sized_for):
+    """A buffer sized for a batch serves smaller ones, down to one token, and
+    nothing behind it is written."""
+    O, I, r = 264, 656, 64
+    nb = lib.theta_workspace_size(lib.THETA_OP_LINEAR_FORWARD_FP8, sized_for, O, I, r, lib.THETA_BF16)
+    buf = torch.full((nb + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    for M in sorted({m for m in (sized_for, 64, 16, 3, 2, 1) if m <= sized_for}, reverse=True):
+        p = Problem(lib, torch, M, O, I, r)
+        p.work = buf[:nb]
+        p.call()
+        lib.theta_device_status()
+        p.check(what=f"{M} of {sized_for} tokens")
+        assert (buf[nb:] == 0xA5).all()
+
+
 def test_outputs_past_32_bit_offsets(lib, torch):
     """Y, and the row encoder's input and codes, of more than 2^31 elements."""
     M, O, I = 131072, 21504, 16
