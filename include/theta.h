@@ -259,7 +259,11 @@ int theta_frob_partials(const void* original, const void* reconstructed, int64_t
  *   X [M, I]; W0 [O, I] (the band's shared block); s fp32 [O]; U [O, rank];
  *   V [I, rank]; Y [M, O], written. Device pointers, dt elements except s.
  *   workspace  device scratch of theta_workspace_size(THETA_OP_LINEAR_FORWARD)
- *              bytes (holds T = X . V); may be NULL when that size is 0.
+ *              bytes (holds T = X . V); may be NULL when that size is 0. For
+ *              THETA_BF16 one or two tokens need 64 * M * rank bytes (partial
+ *              sums), which is more than a few more tokens (31 at most) do: a
+ *              buffer that is to serve every batch up to M tokens takes the
+ *              larger of the sizes for min(M, 2) and for M.
  * THETA_BF16: tensor cores (tcgen05) with fp32 accumulation in tensor memory;
  * T = X.V is kept as a bf16 high part plus a bf16 low part, so the rank-r term
  * carries about 16 significand bits. One or two tokens on a W0 of at most 32M

@@ -213,6 +213,15 @@ def test_gate_up_workspace_covers_both_projections(lib):
     assert lib.theta_workspace_size(lib.THETA_OP_GATE_UP_FORWARD, 16, 64, 64, 0, lib.THETA_BF16) == 0
 
 
+def test_forward_workspace_for_every_batch_up_to_a_size(lib):
+    """The larger of the sizes for min(M, 2) and for M serves every batch up to M tokens."""
+    for dt in (lib.THETA_F32, lib.THETA_BF16):
+        for r in (0, 8, 24, 64, 256):
+            size = [lib.theta_workspace_size(lib.THETA_OP_LINEAR_FORWARD, M, 64, 64, r, dt) for M in range(1, 200)]
+            for M in range(1, 200):
+                assert max(size[:M]) == max(size[min(M, 2) - 1], size[M - 1])
+
+
 def test_workspace_sizes(lib):
     assert lib.theta_workspace_size(lib.THETA_OP_FROB_ERROR, 1, 1, 1, 0, lib.THETA_F32) >= 16
     assert lib.theta_workspace_size(lib.THETA_OP_LINEAR_FORWARD, 16, 256, 256, 0, lib.THETA_F32) == 0
