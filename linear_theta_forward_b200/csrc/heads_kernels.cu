@@ -135,13 +135,38 @@ __device__ __forceinline__ void angle(double turns, float freq, float* c, float*
   *s = quarter & 2 ? -s1 : s1;
 }
 
+// Whether a lane loads its next round of heads while it works on one. The
+// round's registers pay where as many blocks fit an SM with them (65536 /
+// (256 threads x registers)). us without and with, 32 + 8 heads of 256 and
+// 512, 16 + 4 of 1024, 4096 tokens in bf16 and 2048 in fp32 unless noted:
+//   three blocks still, D = 256 bf16   70.2, 67.2 (8192 tokens)
+//   two still, D = 512 bf16            halves 84.1, 75.4
+//   one either way, D = 1024           halves 114, 112 and 82.8, 82.2 (fp32), neighbours 81.8, 73.7 (fp32)
+//   one instead of two, D = 512 fp32   halves 66.5, 78.8, neighbours 63.2, 68.9
+//   one instead of two, D = 1024 bf16  neighbours 84.8, 94.7
+// Halves that cut a vector load the partner value by value and are bound by
+// that, at 124 registers and more: D = 256 81.3, 85.5 (4096 tokens of fp32)
+// and 109, 107 (8192 of bf16), D = 512 138, 150 and 107, 111, D = 1024 in fp32
+// 121, 126; only in bf16 at D = 1024, one head a lane at a time, 254, 178.
+template <typename T, int VPL, int PAIRING>
+constexpr bool fetches_ahead() {
+  if (PAIRING == ODD_HALVES) return VPL == 4 && sizeof(T) == 2;
+  if (VPL == 2) return sizeof(T) == 2;
+  if (VPL == 4) return sizeof(T) == 4 || PAIRING == HALVES;
+  return true;
+}
+
 // G lanes a head, VPL vectors of 8 values a lane.
 template <typename T, int G, int VPL, int PAIRING>
 __global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__ HeadArgs a) {
   extern __shared__ float table[];  // two buffers of [tokens][cos, sin][rotary / 2]
-  // heads a lane loads at once, a round of them ahead of the one worked on
-  // (8192 tokens: 67.2 us; 69.8 and 74.0 with 2 and 4, 70.2 with 4 and none ahead)
-  constexpr int kAhead = VPL == 1 ? 3 : VPL == 2 ? 2 : 1;
+  constexpr bool kFetchAhead = fetches_ahead<T, VPL, PAIRING>();
+  // a partner's vector that another lane holds is loaded with the head's own,
+  // unless those were loaded a round ago: it is in L1 then
+  constexpr bool kPartners = PAIRING == HALVES && VPL > 1 && !kFetchAhead;
+  // heads a lane loads at once (D = 256, 8192 tokens of bf16, a round ahead:
+  // 67.2 us; 69.8 and 74.0 with 2 and 4)
+  constexpr int kAhead = VPL == 1 ? (kFetchAhead ? 3 : 4) : VPL == 2 ? 2 : 1;
   const int64_t* pos = a.pos;
   const float* freq = a.inv_freq;
   pdl_enter(pos, freq);
@@ -232,26 +257,34 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__
           A2[v][q] = pair2(A[v][2 * q], A[v][2 * q + 1]);
           B2[v][q] = pair2(B[v][2 * q], B[v][2 * q + 1]);
         }
-      Raw8<T> raw[kAhead][VPL], ahead[kAhead][VPL];
-      auto fetch = [&](int h0) {
+      Raw8<T> raw[kAhead][VPL], ahead[kFetchAhead ? kAhead : 1][VPL], other[kPartners ? kAhead : 1][VPL];
+      auto fetch = [&](auto& into, int h0) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
           const T* x = x0 + (int64_t)(h0 + u * groups - base) * D;
 #pragma unroll
           for (int v = 0; v < VPL; ++v) {
             const int i0 = (lane + v * G) * 8;
-            ahead[u][v].zero();
-            if (i0 < D && h0 + u * groups < hi) ahead[u][v].load(x + i0);
+            into[u][v].zero();
+            if (i0 < D && h0 + u * groups < hi) into[u][v].load(x + i0);
+            if constexpr (kPartners) {
+              other[u][v].zero();
+              if (i0 < rotary && h0 + u * groups < hi) other[u][v].load(x + (i0 < half ? i0 + half : i0 - half));
+            }
           }
         }
       };
-      fetch(lo + grp);
+      if constexpr (kFetchAhead) fetch(ahead, lo + grp);
       for (int h0 = lo + grp; h0 < hi; h0 += kAhead * groups) {
+        if constexpr (kFetchAhead) {
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
+          for (int u = 0; u < kAhead; ++u)
 #pragma unroll
-          for (int v = 0; v < VPL; ++v) raw[u][v] = ahead[u][v];
-        fetch(h0 + kAhead * groups);
+            for (int v = 0; v < VPL; ++v) raw[u][v] = ahead[u][v];
+          fetch(ahead, h0 + kAhead * groups);
+        } else {
+          fetch(raw, h0);
+        }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
           if (h0 + u * groups >= hi) break;
@@ -270,6 +303,8 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__
               for (int q = 0; q < Raw8<T>::kWords; ++q) o.w[q] = __shfl_sync(mask, raw[u][v].w[q], from, G);
               if (i0 >= rotary) o.zero();
               o.get(p[v]);
+            } else if constexpr (kPartners) {
+              other[u][v].get(p[v]);
             } else if constexpr (PAIRING == HALVES) {
               // in L1: the same head's vectors, loaded by this group of lanes
               Raw8<T> o;
