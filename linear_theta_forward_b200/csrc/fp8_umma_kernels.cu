@@ -398,9 +398,13 @@ constexpr int kPairEpi = 32 * kPairEpiWarps;
 constexpr int kPairThreads = 128 + kPairEpi;
 constexpr uint16_t kPairMask = 0x3;
 static_assert(kPairSf + 2 * 16 <= 512, "accumulators and scales must fit in tensor memory");
-// The copy of group g + 2 to tensor memory overwrites group g's scales: its
-// first stage's load waited for the MMAs kPairStages items back, and group g + 1
-// has at most kGroup items, so group g's MMAs are done.
+// The copy of group g + 2 to tensor memory overwrites group g's scales, so group
+// g's MMAs must be done by then. Between two groups of a tile: g + 1 is full, so
+// the stage of g + 2's first block lies kGroup + 1 blocks behind g's last, and
+// its load waited for the MMAs kPairStages blocks back. A group may be short only
+// as a tile's last one; behind it the issuer waits for the tile's accumulators
+// to have been read (tmem_free), which all of the tile's MMAs precede. A tile
+// that did not wait there (two accumulators in turn) would need a wait of its own.
 static_assert(kPairStages <= kGroup + 1, "a scale group's columns must be free when they are written again");
 static_assert(kPairBBytes % 1024 == 0, "swizzled tiles start on 1024-byte boundaries");
 
@@ -529,6 +533,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     uint32_t ph = 0, ring_ph = 0, free_ph = 1;
     for (int tile = cluster; tile < tiles && !stop; tile += n_clusters) {
       // the epilogues of both CTAs have read the previous tile's accumulators
+      // (its last scale groups are done with too)
       bool ok = !any || ptx::mbar_wait(tmem_free, free_ph, abort_flag);
       free_ph ^= 1u;
       const int N = tile_n(tile);

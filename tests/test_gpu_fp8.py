@@ -308,6 +308,22 @@ def test_work_after_a_timeout_is_flagged_then_recovers(lib, torch, M):
     p.check()
 
 
+@pytest.mark.parametrize("M,O,r", [(1000, 8200, 0), (1000, 8200, 8), (300, 21504, 0)])
+@pytest.mark.parametrize("I", [16, 272, 512, 640, 656, 896, 1168])
+def test_scale_groups_over_several_tiles_of_a_cluster(lib, torch, M, O, r, I):
+    """More CTA-pair tiles than pairs, with and without a rank term between
+    them, the last scale group of a tile of 1 to 4 blocks; every block of W0
+    and every token's block has a scale far from its neighbours', so that one
+    used for another shows."""
+    p = Problem(lib, torch, M, O, I, r)
+    g = torch.Generator(device="cuda").manual_seed(I)
+    for scales in (p.xs, p.ws):
+        scales.copy_(torch.randint(117, 138, scales.shape, device="cuda", generator=g))
+    p.call()
+    lib.theta_device_status()
+    p.check(what=f"{M}x{O}x{I} r{r}")
+
+
 @pytest.mark.parametrize("sized_for", [2, 3, 16, 64, 300])
 def test_one_workspace_for_a_batch_that_shrinks(lib, torch, sized_for):
     """A buffer sized for a batch serves smaller ones, down to one token, and
