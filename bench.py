@@ -262,15 +262,17 @@ def summarize(stages, stage_ms, step_ms, peaks):
 
 
 # The main kernel behind each group of stages, and the sources that define it
-# and its launch code (shared device helpers included): a recorded ncu traffic
-# figure stands only while these files hash to the value recorded beside it.
+# and its launch code, every local header that they include among them: a
+# recorded ncu traffic figure stands only while these files hash to the value
+# recorded beside it.
 KIND_SOURCES = {
-    "prelude": ["prelude_kernels.cu", "stream_kernels.cu", "common.cuh", "umma_ptx.cuh"],
-    "reconstruct": ["umma_kernels.cu", "umma_ptx.cuh", "common.cuh"],
-    "frob": ["stream_kernels.cu", "common.cuh"],
-    "forward_decode": ["gemv_kernels.cu", "umma_kernels.cu", "umma_ptx.cuh", "common.cuh"],
-    "forward_ridge": ["umma_kernels.cu", "umma_ptx.cuh", "common.cuh"],
-    "forward_prefill": ["umma_kernels.cu", "umma_ptx.cuh", "common.cuh"],
+    "prelude": ["prelude_kernels.cu", "stream_kernels.cu", "common.cuh", "internal.h", "umma_ptx.cuh"],
+    "reconstruct": ["umma_kernels.cu", "umma_host.cuh", "umma_ptx.cuh", "common.cuh", "internal.h"],
+    "frob": ["stream_kernels.cu", "common.cuh", "internal.h"],
+    "forward_decode": ["gemv_kernels.cu", "umma_kernels.cu", "umma_host.cuh", "umma_ptx.cuh", "common.cuh",
+                       "internal.h"],
+    "forward_ridge": ["umma_kernels.cu", "umma_host.cuh", "umma_ptx.cuh", "common.cuh", "internal.h"],
+    "forward_prefill": ["umma_kernels.cu", "umma_host.cuh", "umma_ptx.cuh", "common.cuh", "internal.h"],
 }
 KERNEL_NAMES = {
     "prelude": "prelude_pipe_kernel / prelude_band2_kernel (+ band_mean_kernel)",

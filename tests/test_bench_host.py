@@ -149,6 +149,18 @@ def test_traffic_sources_exist_and_gate_the_figure(tmp_path, monkeypatch):
         assert bench.recorded_traffic("prelude", "C1") is None or stamp == now
 
 
+def test_traffic_sources_list_every_header_they_include():
+    """A local header that a listed source includes decides its kernels' traffic as well."""
+    import re
+    csrc = os.path.join(ROOT, "linear_theta_forward_b200", "csrc")
+    for kind, files in bench.KIND_SOURCES.items():
+        for f in files:
+            with open(os.path.join(csrc, f)) as src:
+                used = re.findall(r'^#include "([^"]+)"', src.read(), re.M)
+            missing = [h for h in used if os.path.exists(os.path.join(csrc, h)) and h not in files]
+            assert not missing, (kind, f, missing)
+
+
 def test_oracle_sample_is_bounded_and_counts_bytes():
     """The CPU baseline's sample runs every config's stages on a few rows and
     reports the bytes of exactly what it ran."""
