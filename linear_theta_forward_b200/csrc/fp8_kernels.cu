@@ -135,10 +135,6 @@ __device__ __noinline__ uint2 encode_checked(const Raw8<T>& r, float inv) {
   return make_uint2(encode4(v[0], v[1], v[2], v[3]), encode4(v[4], v[5], v[6], v[7]));
 }
 
-// One CTA per 128 x 128 block of W0: a thread holds 8 vectors of 8 values
-// (rows t / 16 + 16 j), so the block is read once, with all its loads in
-// flight, and written from registers. [21504, 5376] in bf16: 52.5 us, 6.6
-// TB/s, the rate of a plain copy.
 // The largest magnitude of the CTA's values: `mx` reduced over its threads.
 __device__ __forceinline__ float cta_max(float mx, float* red) {
 #pragma unroll
@@ -150,6 +146,10 @@ __device__ __forceinline__ float cta_max(float mx, float* red) {
   return mx;
 }
 
+// One CTA per 128 x 128 block of W0: a thread holds 8 vectors of 8 values
+// (rows t / 16 + 16 j), so the block is read once, with all its loads in
+// flight, and written from registers. [21504, 5376]: 53 us in bf16, 86 in fp32,
+// 6.6 and 6.7 TB/s, the rate of a plain copy.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
 fp8_quantize_kernel(const T* __restrict__ W, int64_t O, int64_t I, uint8_t* __restrict__ codes,
@@ -230,9 +230,10 @@ __device__ __forceinline__ void group_max(const Raw8<float>& a, const Raw8<float
 // blocks of the token in flight per lane. A CTA's 16 groups of lanes take up to
 // 16 tokens (1 << row_bits) side by side, so that a block's scales, which lie
 // token by token, leave as runs of bytes: with all 16 groups on one token they
-// were single bytes, a sector each. [2048, 21504] in bf16: 25.8 us, 5.1 TB/s,
-// 74% of the issue slots used; one token of 5376 1.5 us (2.9 with eight blocks
-// a lane, which bf16 rows did not gain from either: 29.6).
+// were single bytes, a sector each. [2048, 21504]: 25.8 us in bf16, 5.1 TB/s,
+// 74% of the issue slots used, and 47 in fp32, 4.7 TB/s; one token of 5376 1.5
+// us (2.9 with eight blocks a lane, which bf16 rows did not gain from either:
+// 29.6).
 constexpr int kRowBlocks = 2;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) fp8_quantize_rows_kernel(const T* __restrict__ X, int64_t M, int64_t I,

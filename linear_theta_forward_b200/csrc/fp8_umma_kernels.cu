@@ -704,9 +704,15 @@ struct Maps {
 
 // K splits of the one-SM tiles: while every SM still gets at most one CTA and
 // each split keeps 8 K blocks; below that the sum over the cluster costs more
-// than the shorter walk saves (128 tokens of [1152, 6912], 54 blocks: 23.2 us
-// unsplit, 16.1, 12.0 and 14.7 with 2, 4 and 8 splits; one token of [6912,
-// 1152], 9 blocks: 8.7 and 9.3 with 1 and 2).
+// than the shorter walk saves. us with 1, 2, 4 and 8 splits (* this rule's):
+//     1 token of  [6912, 1152]     6.9*  7.9   8.1  14.5     9 blocks
+//   128 tokens of [1152, 6912]    23.1  15.9  11.7* 14.5    54 blocks
+//     1 token of  [21504, 5376]   24.2* 30.3  33.8  54.8   168 tiles
+//    16 tokens of [8192, 5376]    19.1  14.8* 14.4  21.0    64 tiles
+//    16 tokens of [5376, 8192]    25.2  17.3* 15.2  14.8    42 tiles
+//    16 tokens of [5376, 21504]   56.5  34.0* 25.9  25.4    42 tiles, 168 blocks
+// The last two are where it stops early: a power of two leaves 84 CTAs, and
+// behind a long walk a second CTA of an SM would pay.
 int tile_splits(const LaunchCtx& c, int64_t m_tiles, int64_t n_tiles, int kb) {
   int s = 1;
   if (c.policy != THETA_POLICY_THROUGHPUT)
@@ -772,13 +778,16 @@ int launch_forward_fp8(const LaunchCtx& c, const void* X, const void* xq, const 
     if ((st = launch_xv_umma(c, X, V, M, I, r, t_hi, t_lo, ce))) return st;
   }
   const int width = (int)(ceil_div(ceil_div(M, ceil_div(M, kPairN)), 16) * 16);  // tokens of a pair's tile
-  // 64 tokens a tile at most on one SM: wider tiles leave SMs without work or
-  // cost splits (333 tokens of [2056, 1168]: 13.2 us against 16.3 with 128)
+  // 64 tokens a tile at most on one SM: wider tiles leave SMs without work (128
+  // tokens of [1152, 6912], K split 4 ways: 11.7 us, 14.5 with 128)
   const int BN = M <= 16 ? 16 : M <= 32 ? 32 : 64;
   // More than 64 tokens: CTA pairs, which load less per product, unless the
-  // one-SM tiles are so few that they split K (us, one-SM and pairs: 2048
-  // tokens of [21504, 5376] 424 and 254; 128 tokens of [8192, 5376] 22.7 and
-  // 22.0; 100 tokens of [1152, 6912] 11.6 and 22.9).
+  // one-SM tiles are so few that they split K. us, one-SM and pairs (* this
+  // rule's): 2048 tokens of [21504, 5376] 416, 245*; 128 of it 44.7, 39.9*; 333
+  // of [2056, 1168] 12.7, 12.3*; 256 of [5376, 8192] 30.2, 28.0*; 100 of [1152,
+  // 6912] 11.6*, 22.5. It asks for a split that the tiles could take on SMs of
+  // their own; with one they cannot, 128 tokens of [8192, 5376] take 19.4 (2
+  // ways), 21.7*, of [5376, 8192] 21.5, 27.6*, of [5376, 21504] 40.1, 57.6*.
   const bool pair = M > 64 && tile_splits(c, ceil_div(O, kBM), ceil_div(M, 64), (int)ceil_div(I, kBK)) == 1;
   const int box = pair ? width / 2 : BN;  // tokens per box
   Maps mp;

@@ -371,7 +371,11 @@ cudaError_t launch_heads(const LaunchCtx& c, HeadArgs a) {
   const int heads = a.side[0].heads + a.side[1].heads;
   // Few tokens: a block a token and pass of heads, so that the heads spread
   // over the GPU. Many: two warps a token, which share its angles and factors
-  // over more heads, in one wave of blocks.
+  // over more heads, in one wave of blocks. us, few and many, at 148, 222, 295
+  // and 296 tokens (148 SMs): 32 + 8 heads of 256 in bf16 6.0, 7.9; 8.1, 7.9;
+  // 10.3, 7.9; 10.3, 7.9; 4 + 1 heads of 256 3.4, 3.9; 3.8, 3.9; 4.3, 3.9; 4.3,
+  // 3.9; 32 + 8 heads of 512 in fp32 11.2, 16.1; 16.2, 19.4; 20.8, 20.4; 20.9,
+  // 20.5.
   const bool few = a.M < 2 * (int64_t)c.num_sms;
   a.warps = few ? kWarps : 2;
   a.per_block = few ? std::min(heads, kThreads / G) : heads;
