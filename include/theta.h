@@ -30,6 +30,8 @@
  *     context current. Pointers and the stream belong to that context. At most
  *     64 contexts of a process can call the library over its life
  *     (THETA_ERR_UNSUPPORTED).
+ *   - A workspace is written by the call: calls that may run at the same time
+ *     (on different streams, in different graphs) need one each.
  *   - THETA_BF16 calls use the Tensor Memory Accelerator and need 16-byte
  *     aligned base pointers and row pitches that are multiples of 16 bytes
  *     (I, O and r multiples of 8); otherwise they return THETA_ERR_ALIGNMENT.

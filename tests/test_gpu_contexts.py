@@ -158,12 +158,36 @@ for c, case in zip(contexts, cases):
 }
 
 
-def run_case(code):
+def run_case(code, limit=120):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-    done = subprocess.run([sys.executable, "-c", COMMON + code], cwd=root, timeout=120, capture_output=True, text=True)
+    done = subprocess.run([sys.executable, "-c", COMMON + code], cwd=root, timeout=limit, capture_output=True, text=True)
     assert done.returncode == 0, done.stderr[-2000:]
 
 
 @pytest.mark.parametrize("what", list(CASES))
 def test_context_of_a_call(what):
     run_case(CASES[what])
+
+
+LAST = """
+P = vp(4096)
+call = lambda: raw.theta_linear_forward_nvfp4(P, 1, 1 << 20, P, P, P, 8, P, None, None, 0, P, None, 0, None)
+first = create()
+case = Case(30)
+case.run()
+for n in range(64):
+    c = create()
+    assert call() == -2
+    assert ("contexts" in th.theta_last_error()) == (n == 63), (n, th.theta_last_error())
+    assert current() == c.value
+    ok(cu.cuCtxDestroy_v2(c))
+    ok(cu.cuCtxSetCurrent(first))
+case.run()
+"""
+
+
+@pytest.mark.slow
+def test_context_after_the_last_is_refused():
+    """64 contexts are served and the next one refused, with the first still
+    served (each context loads the library's kernels: about 45 s)."""
+    run_case(LAST, limit=600)
